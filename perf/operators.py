@@ -453,14 +453,14 @@ def _run_own(s):
         else:
             out, rstd = s["out"], s["rstd"]
         got = ssd.add_rms_norm_backward(s["dy"], out, s["weight"], rstd, dresidual_out=s["dout"],
-                                        x=None if s["scale"] is None else s["x"], scale=s["scale"], x_dtype=t)
+                                        x=None if s["scale"] is None else s["x"], scale=s["scale"])
         got = dict(zip(("dx", "dresidual", "dweight", "dscale"), got))
         return got if op == "residual-backward" else {"y": y, "out": out, **got}
     if op in ("gate", "gate-train"):
         kind = {"groups": case["groups"], "norm_before_gate": case["norm_first"]}
         if op == "gate":
-            return {"y": ssd.gated_rms_norm(s["x"], s["z"], s["weight"], eps=EPS, y_dtype=t, **kind)}
-        y, rstd = ssd.gated_rms_norm(s["x"], s["z"], s["weight"], eps=EPS, y_dtype=t, want_rstd=True, **kind)
+            return {"y": ssd.gated_rms_norm(s["x"], s["z"], s["weight"], eps=EPS, **kind)}
+        y, rstd = ssd.gated_rms_norm(s["x"], s["z"], s["weight"], eps=EPS, want_rstd=True, **kind)
         dx, dz, dweight = ssd.gated_rms_norm_backward(s["dy"], s["x"], s["z"], s["weight"], rstd, **kind)
         return {"y": y, "dx": dx, "dz": dz, "dweight": dweight}
     dx, dweight, dbias, dstate = ssd.causal_conv1d_backward(s["dys"], s["x"], s["weight"], s["bias"], cu_seqlens=cu,
