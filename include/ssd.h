@@ -368,6 +368,222 @@ ssd_status ssd_chunked_scan_noalloc(const void* x, const float* dt, const float*
                                     const float* init_state, void* y, float* final_state,
                                     const ssd_shape* shape, void* stream);
 
+/*
+ * Gradients of ssd_causal_conv1d: with v the pre-activation of the forward
+ * pass (recomputed here) and dv = dout silu'(v) (dv = dout without activation),
+ *
+ *     dx[t, c]      = sum_k weight[c, k] dv[t + K-1-k, c]     (inside the sequence)
+ *     dweight[c, k] = sum_t dv[t, c] xp[t + k, c],   dbias[c] = sum_t dv[t, c]
+ *
+ * and, for the conv states, dstate_in from the tokens that read it; the
+ * gradient dstate_out of the final state is added to the last K-1 rows of
+ * xp, wherever they come from.
+ *
+ *   x, weight, bias, conv_state_in, shape   as given to ssd_causal_conv1d
+ *   dout          the output parts' gradients, [rows, channels[p]] in ydtype
+ *                 (the parts of the forward call; read only)
+ *   dstate_out    [batch, K-1, C]  dtype, or NULL (zero)
+ *   dx            [rows, C]        dtype
+ *   dweight       [C, K]           fp32
+ *   dbias         [C]              fp32, or NULL (not written)
+ *   dstate_in     [batch, K-1, C]  dtype, or NULL (not written)
+ *   workspace     device scratch of the queried size (16-byte aligned),
+ *                 contents undefined on entry and exit
+ * Sums over tokens are fp32, in an order that depends on the shape alone.
+ * Rows of a packed batch behind the last sequence (cu_seqlens[batch] < T) are
+ * not read and not written; the host copy, where given, may end before T.
+ * No output may alias an input or another output.  Errors as
+ * ssd_causal_conv1d, plus SSD_ERR_WORKSPACE.
+ */
+ssd_status ssd_causal_conv1d_backward_workspace_size(const ssd_conv_shape* shape, size_t* bytes);
+
+ssd_status ssd_causal_conv1d_backward(const ssd_conv_outputs* dout, const void* x, const float* weight,
+                                      const float* bias, const void* conv_state_in, const void* dstate_out,
+                                      void* dx, float* dweight, float* dbias, void* dstate_in,
+                                      const ssd_conv_shape* shape, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Gated linear recurrence, per sequence, channel c and token t:
+ *
+ *     log a_t = -rate softplus(lam[c]) sigmoid(r[t, c])
+ *     h_t     = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i[t, c]) x[t, c]
+ *     y[t, c] = h_t
+ *
+ * the diagonal recurrence of the scan above with one state per channel and
+ * both gates taken from the token: the recurrent layer's x, r and i are three
+ * projections of its input (often column ranges of one buffer, hence the row
+ * strides).  The state is fp32.
+ *
+ * Shape:
+ *   batch, seqlen, cu_seqlens, cu_seqlens_host   dense or packed, as
+ *                ssd_conv_shape; rows < 2^31
+ *   channels     C, a multiple of 8, at most 2^20
+ *   dtype        ssd_dtype of x, r, i (and dx, dr, di)
+ *   ydtype       ssd_dtype of y (and dy)
+ *   rate         finite and > 0
+ *   x_stride, r_stride, i_stride      elements from one row to the next:
+ *                multiples of 8, at least C; 0 means C
+ *   dx_stride, dr_stride, di_stride   the same for the gradients (backward only)
+ *   reserved     must be 0
+ * A packed batch may hold rows behind its last sequence (cu_seqlens[batch] <
+ * seqlen): they are not read into any result and not written.  A sequence
+ * without tokens passes its state (and its gradient) through.
+ */
+typedef struct ssd_gated_shape {
+    int64_t batch;
+    int64_t seqlen;
+    int32_t channels;
+    int32_t dtype;
+    int32_t ydtype;
+    float rate;
+    int64_t x_stride, r_stride, i_stride;
+    int64_t dx_stride, dr_stride, di_stride;
+    int64_t reserved;
+    const int32_t* cu_seqlens;      /* device int32 [batch+1], or NULL (dense) */
+    const int32_t* cu_seqlens_host; /* optional host copy; validated when given */
+} ssd_gated_shape;
+
+/*
+ * Rows of the saved states: the forward pass can keep the fp32 state entering
+ * every SSD_GATED_TILE_ROWS rows of the batch's rows, [states_rows, C] with
+ * states_rows = ceil(rows / SSD_GATED_TILE_ROWS); the backward pass needs it.
+ */
+#define SSD_GATED_TILE_ROWS 128
+
+/* Workspace bytes of ssd_gated_scan (backward = 0) or _backward (1). */
+ssd_status ssd_gated_scan_workspace_size(const ssd_gated_shape* shape, int32_t backward, size_t* bytes);
+
+/*
+ *   x, r, i      [rows, C]      dtype
+ *   lam          [C]            fp32
+ *   init_state   [batch, C]     fp32, or NULL (zero)
+ *   y            [rows, C]      ydtype
+ *   final_state  [batch, C]     fp32, or NULL (not written); not init_state
+ *   states       [states_rows, C] fp32, or NULL (not written)
+ *   workspace    device scratch of the queried size, 16-byte aligned,
+ *                contents undefined on entry and exit
+ * No output may alias an input or another output.
+ * Errors: SSD_ERR_NULL, SSD_ERR_ALIGN, SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes,
+ * strides, aliasing), SSD_ERR_VALUE (rate), SSD_ERR_SEQLENS,
+ * SSD_ERR_WORKSPACE, SSD_ERR_HIP.
+ */
+ssd_status ssd_gated_scan(const void* x, const void* r, const void* i, const float* lam, const float* init_state,
+                          void* y, float* final_state, float* states, const ssd_gated_shape* shape,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of ssd_gated_scan for dy [rows, C] (ydtype) and dfinal_state
+ * [batch, C] fp32 (or NULL, zero):
+ *   dx, dr, di   [rows, C]  dtype
+ *   dlam         [C]        fp32 (summed in fp32, in an order that depends on
+ *                           the shape alone)
+ *   dinit_state  [batch, C] fp32, or NULL (not written); not dfinal_state
+ * x, r, i, lam, init_state, shape as given to the forward pass, states as
+ * written by it.  Same errors.
+ */
+ssd_status ssd_gated_scan_backward(const void* dy, const float* dfinal_state, const void* x, const void* r,
+                                   const void* i, const float* lam, const float* init_state,
+                                   const float* states, void* dx, void* dr, void* di, float* dlam,
+                                   float* dinit_state, const ssd_gated_shape* shape, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * One token per sequence: x, r, i [batch, C]; state [batch, C] fp32 is read
+ * and state_out (which may be state) written; y [batch, C] in ydtype.
+ * shape->seqlen, cu_seqlens and the gradients' strides are ignored.
+ */
+ssd_status ssd_gated_scan_step(const float* state, float* state_out, const void* x, const void* r, const void* i,
+                               const float* lam, void* y, const ssd_gated_shape* shape, void* stream);
+
+/*
+ * RMS norms around a block.  A row (or each of its `groups` equal column
+ * ranges) is divided by its root mean square; eps is finite and >= 0:
+ *     rstd = 1 / sqrt(mean(v^2) + eps)
+ *
+ * Residual norm (in front of a block, with the residual addition of the block
+ * before and its scale per column):
+ *     out = residual + scale x            (scale NULL: residual + x)
+ *     y   = out rstd weight
+ * y and rstd come from the fp32 sum, out is that sum rounded to its type.
+ *
+ * Gated norm (behind the scan, z the gate's input):
+ *     norm_before_gate 0:  v = x silu(z),  y = v rstd weight
+ *     norm_before_gate 1:  v = x,          y = v rstd weight silu(z)
+ *
+ * Shape:
+ *   rows         >= 0; rows * groups < 2^31
+ *   columns      D, a multiple of 8 * groups; at most 16384 columns a group
+ *                (SSD_ERR_UNSUPPORTED above)
+ *   groups       1 for the residual norm; at most 1024
+ *   dtype        ssd_dtype of the block's stream: residual norm x and y, gated
+ *                norm z and y
+ *   dtype2       ssd_dtype of the residual and out, or of the gated norm's x:
+ *                dtype, or SSD_F32 (SSD_ERR_UNSUPPORTED: fp32 with bf16)
+ *   eps, norm_before_gate (0 for the residual norm)
+ *   x_stride, z_stride, dx_stride, dz_stride   gated norm: row strides of x, z
+ *                and their gradients in elements (multiples of 8, at least D; 0
+ *                means D); 0 for the residual norm
+ *   reserved     must be 0
+ */
+typedef struct ssd_norm_shape {
+    int64_t rows;
+    int32_t columns;
+    int32_t groups;
+    int32_t dtype;
+    int32_t dtype2;
+    float eps;
+    int32_t norm_before_gate;
+    int64_t x_stride, z_stride, dx_stride, dz_stride;
+    int64_t reserved;
+} ssd_norm_shape;
+
+/* Workspace bytes of the backward passes below. */
+ssd_status ssd_norm_backward_workspace_size(const ssd_norm_shape* shape, size_t* bytes);
+
+/*
+ *   x          [rows, D]  dtype
+ *   residual   [rows, D]  dtype2
+ *   weight     [D]        fp32
+ *   scale      [D]        fp32, or NULL
+ *   y          [rows, D]  dtype
+ *   out        [rows, D]  dtype2; may be residual
+ *   rstd       [rows]     fp32, or NULL (not written); the backward pass takes it
+ */
+ssd_status ssd_add_rms_norm(const void* x, const void* residual, const float* weight, const float* scale, void* y,
+                            void* out, float* rstd, const ssd_norm_shape* shape, void* stream);
+
+/*
+ * For the gradients dy of y and dout of out (dtype2, or NULL for zero):
+ *     dresidual = dout + rstd (weight dy - m mean(weight dy m)),  m = out rstd
+ *     dx = scale dresidual,  dweight = sum over rows of dy m,
+ *     dscale = sum over rows of dresidual x
+ *   dx         [rows, D]  dtype; may be dout where the two dtypes are one
+ *   dresidual  [rows, D]  dtype2, or NULL (not written: without a scale and
+ *              with one dtype dx is it); may be dout
+ *   dweight    [D] fp32
+ *   dscale     [D] fp32, or NULL (not written); needs scale and x
+ * Sums over rows are fp32, in an order that depends on the shape alone.
+ */
+ssd_status ssd_add_rms_norm_backward(const void* dy, const void* dout, const void* out, const float* weight,
+                                     const float* rstd, const void* x, const float* scale, void* dx,
+                                     void* dresidual, float* dweight, float* dscale, const ssd_norm_shape* shape,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ *   x          [rows, D]  dtype2     z  [rows, D]  dtype
+ *   weight     [D] fp32              y  [rows, D]  dtype
+ *   rstd       [rows, groups] fp32, or NULL (not written)
+ */
+ssd_status ssd_gated_rms_norm(const void* x, const void* z, const float* weight, void* y, float* rstd,
+                              const ssd_norm_shape* shape, void* stream);
+
+/* dy [rows, D] dtype; dx dtype2, dz dtype [rows, D]; dweight [D] fp32. */
+ssd_status ssd_gated_rms_norm_backward(const void* dy, const void* x, const void* z, const float* weight,
+                                       const float* rstd, void* dx, void* dz, float* dweight,
+                                       const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
 /* Static English name of a status code. */
 const char* ssd_status_string(int32_t status);
 

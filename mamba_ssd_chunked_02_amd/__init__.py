@@ -21,7 +21,9 @@ import os
 from typing import Optional, Sequence, Tuple
 
 __all__ = ["chunked_scan", "chunked_scan_noalloc", "decode_step", "decode_window_step", "causal_conv1d",
-           "conv1d_step", "workspace_size", "SsdError", "library_path", "load"]
+           "conv1d_step", "workspace_size", "SsdError", "library_path", "load", "gated_scan", "gated_scan_step",
+           "gated_scan_backward", "add_rms_norm", "add_rms_norm_backward", "gated_rms_norm",
+           "gated_rms_norm_backward", "causal_conv1d_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libssd_mi355x.so"
@@ -525,3 +527,7 @@ def conv1d_step(conv_state, x, weight, bias=None, *, activation: bool = True,
                                        ctypes.byref(sh), _stream_handle(x))
     _check(st, "ssd_causal_conv1d_step")
     return outs
+
+
+from .block_ops import (add_rms_norm, add_rms_norm_backward, causal_conv1d_backward, gated_rms_norm,  # noqa: E402
+                        gated_rms_norm_backward, gated_scan, gated_scan_backward, gated_scan_step)

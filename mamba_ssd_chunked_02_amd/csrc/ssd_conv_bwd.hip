@@ -1,0 +1,283 @@
+// Gradients of the causal depthwise conv1d (+ SiLU) on gfx950.  With
+// v[t] = bias + sum_k w[k] xp[t + k] over the padded sequence
+// xp = [conv state (K-1 rows); x] and out = silu(v):
+//   dv[t]  = dy[t] silu'(v[t])                      (v recomputed from x)
+//   dx[t]  = sum_k w[k] dv[t + K-1-k]               (inside the sequence)
+//   dw[k]  = sum_t dv[t] xp[t + k],   db = sum_t dv[t]
+// and what the final conv state's gradient adds to the last K-1 inputs.
+// About 6K + 12 operations per element: an HBM stream (x and dy in, dx out).
+//
+// A lane owns 4 consecutive channels and walks a block of rows in batches of
+// kBatch; the K-1 inputs and the K-1 dv around a batch stay in registers.
+// The rows just behind a block, whose dv its last dx need, are computed again
+// by the block behind (K-1 rows in block_rows).  A batch that touches no
+// sequence boundary takes a path with no test per row.
+#include <algorithm>
+#include <type_traits>
+
+#include "ssd_gated.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kBwdThreads = 256;
+constexpr int kBatch = 8;
+constexpr int kCh = 4;
+constexpr int kWaveCh = 64 * kCh;
+
+template <typename Y>
+struct Part {
+    const Y* p;
+    int64_t stride;
+};
+
+// The gradient of the lane's 4 channels in row 0, and its row stride.
+template <typename Y>
+__device__ inline Part<Y> dy_part(const ConvBwdArgs& a, int c0) {
+    int off = 0;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        if (p + 1 < a.nparts && c0 >= off + a.part_ch[p]) off += a.part_ch[p];
+        else return {(const Y*)a.dy[p] + (c0 - off), a.part_ch[p]};
+    }
+    return {(const Y*)a.dy[2] + (c0 - off), a.part_ch[2]};
+}
+
+template <int K>
+struct Taps4 {
+    f32x4 w[K], b;
+};
+
+template <int K>
+__device__ inline Taps4<K> load_taps4(const ConvBwdArgs& a, int c0) {
+    Taps4<K> t;
+#pragma unroll
+    for (int c = 0; c < kCh; ++c)
+#pragma unroll
+        for (int k = 0; k < K; ++k) t.w[k][c] = a.weight[(int64_t)(c0 + c) * K + k];
+    t.b = a.bias ? *(const f32x4*)(a.bias + c0) : f32x4{};
+    return t;
+}
+
+// dv of one row from its K inputs and dy.
+template <int K, bool SILU>
+__device__ inline f32x4 dv_row(const Taps4<K>& t, const f32x4* h, f32x4 dy) {
+    if constexpr (!SILU) return dy;
+    f32x4 v = t.b;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v += t.w[k] * h[k];
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) {
+        const float s = sigmoid_f(v[c]);
+        dy[c] *= s * (1.f + v[c] * (1.f - s));
+    }
+    return dy;
+}
+
+// The input j rows into the padded sequence [lo - (K-1), hi).
+template <typename T, int K>
+__device__ inline f32x4 padded_input(const ConvBwdArgs& a, int64_t s, RowRange q, int64_t j, int c0) {
+    if (j < K - 1) return a.state_in ? Tr<T>::ld4((const T*)a.state_in + (s * (K - 1) + j) * a.C + c0) : f32x4{};
+    return Tr<T>::ld4((const T*)a.x + (q.lo + j - (K - 1)) * a.C + c0);
+}
+
+template <typename T, typename Y, int K, bool SILU>
+__global__ __launch_bounds__(kBwdThreads) void conv_backward_kernel(ConvBwdArgs a) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int c = blockIdx.y * kWaveCh + lane * kCh;
+    const bool on = c < a.C;
+    const int c0 = on ? c : a.C - kCh;
+    const int rows = a.block_rows / 4;  // rows of a wave
+    const int64_t r0 = min((int64_t)blockIdx.x * a.block_rows + wave * rows, a.T), r1 = min(r0 + rows, a.T);
+    const RowRange live = live_rows(a.cu, a.nseq, a.T);
+    const Taps4<K> tp = load_taps4<K>(a, c0);
+    const Part<Y> dyp = dy_part<Y>(a, c0);
+    const T* xb = (const T*)a.x + c0;
+    T* dxb = (T*)a.dx + c0;
+    f32x4 dw[K] = {}, db = {};
+
+    // One row by itself, for rows around a sequence boundary: its K inputs
+    // (from the state before its first token) and its dv.
+    struct Alone {
+        f32x4 h[K], dv;
+    };
+    auto alone = [&](int64_t t, int64_t s, RowRange q) {
+        Alone r;
+#pragma unroll
+        for (int k = 0; k < K; ++k) r.h[k] = padded_input<T, K>(a, s, q, t - q.lo + k, c0);
+        r.dv = dv_row<K, SILU>(tp, r.h, Tr<Y>::ld4(dyp.p + t * dyp.stride));
+        return r;
+    };
+
+    int64_t s = -1;
+    RowRange q = {0, 0};  // the sequence holding the current row
+    for (int64_t rb = r0; rb < r1; rb += kBatch) {
+        const int64_t re = min(rb + kBatch, r1);
+        if (rb >= q.hi && rb >= live.lo && rb < live.hi) {
+            s = seq_of(a.cu, a.nseq, a.L, rb);
+            q = seq_range(a.cu, a.L, a.T, s);
+        }
+        if (re - rb == kBatch && rb - (K - 1) >= q.lo && re + K - 1 <= q.hi) {
+            f32x4 h[kBatch + 2 * (K - 1)], dv[kBatch + K - 1];
+            typename Tr<Y>::v4 dy[kBatch + K - 1];
+#pragma unroll
+            for (int j = 0; j < kBatch + 2 * (K - 1); ++j) h[j] = Tr<T>::ld4(xb + (rb + j - (K - 1)) * a.C);
+#pragma unroll
+            for (int j = 0; j < kBatch + K - 1; ++j) dy[j] = Tr<Y>::ld4raw(dyp.p + (rb + j) * dyp.stride);
+#pragma unroll
+            for (int j = 0; j < kBatch + K - 1; ++j) dv[j] = dv_row<K, SILU>(tp, h + j, Tr<Y>::widen4(dy[j]));
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                f32x4 dx = {};
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    dx += tp.w[k] * dv[j + K - 1 - k];
+                    dw[k] += dv[j] * h[j + k];
+                }
+                db += dv[j];
+                if (on) Tr<T>::st4(dxb + (rb + j) * a.C, dx);
+            }
+            continue;
+        }
+        for (int64_t t = max(rb, live.lo); t < min(re, live.hi); ++t) {
+            if (t >= q.hi || t < q.lo) {
+                s = seq_of(a.cu, a.nseq, a.L, t);
+                q = seq_range(a.cu, a.L, a.T, s);
+                if (t < q.lo || t >= q.hi) continue;  // an invalid offset list
+            }
+            const Alone r = alone(t, s, q);
+            db += r.dv;
+            f32x4 dx = tp.w[K - 1] * r.dv;
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k] += r.dv * r.h[k];
+            for (int d = 1; d < K && t + d < q.hi; ++d) {
+                const Alone n = alone(t + d, s, q);
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (k == K - 1 - d) dx += tp.w[k] * n.dv;
+            }
+            // the final state holds the last K-1 inputs
+            if (a.dstate_out && t >= q.hi - (K - 1))
+                dx += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + t - (q.hi - (K - 1))) * a.C + c0);
+            if (on) Tr<T>::st4(dxb + t * a.C, dx);
+        }
+    }
+    // the workgroup's sums: waves 1..3 through LDS, added in order
+    __shared__ f32x4 sums[3][K + 1][64];
+    if (wave) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) sums[wave - 1][k][lane] = dw[k];
+        sums[wave - 1][K][lane] = db;
+    }
+    __syncthreads();
+    if (wave || !on) return;
+#pragma unroll
+    for (int k = 0; k <= K; ++k) {
+        f32x4 v = k < K ? dw[k < K ? k : 0] : db;
+#pragma unroll
+        for (int o = 0; o < 3; ++o) v += sums[o][k][lane];
+        *(f32x4*)(a.part + ((int64_t)blockIdx.x * (K + 1) + k) * a.C + c0) = v;
+    }
+}
+
+// Gradient of the incoming state: row j of it is an input of the tokens t < j + 1,
+//   dstate[j] = sum over k <= j, j - k < length of w[k] dv[j - k],
+// plus the final state's own gradient where the sequence is too short to
+// have pushed the row out.
+template <typename T, typename Y, int K, bool SILU>
+__global__ __launch_bounds__(kBwdThreads) void conv_backward_state_kernel(ConvBwdArgs a) {
+    const int64_t quads = a.C / kCh, id = (int64_t)blockIdx.x * kBwdThreads + threadIdx.x;
+    if (id >= a.nseq * quads) return;
+    const int64_t s = id / quads;
+    const int c0 = (int)(id - s * quads) * kCh;
+    const RowRange q = seq_range(a.cu, a.L, a.T, s);
+    const int64_t len = q.hi - q.lo;
+    const Taps4<K> tp = load_taps4<K>(a, c0);
+    const Part<Y> dyp = dy_part<Y>(a, c0);
+    f32x4 ds[K - 1] = {};
+#pragma unroll
+    for (int t = 0; t < K - 1; ++t) {
+        if (t >= len) break;
+        f32x4 h[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) h[k] = padded_input<T, K>(a, s, q, t + k, c0);
+        const f32x4 dv = dv_row<K, SILU>(tp, h, Tr<Y>::ld4(dyp.p + (q.lo + t) * dyp.stride));
+#pragma unroll
+        for (int k = 0; k + t < K - 1; ++k) ds[t + k] += tp.w[k] * dv;
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        // row j of the padded sequence is row j - len of the final state
+        if (a.dstate_out && j >= len)
+            ds[j] += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + j - len) * a.C + c0);
+        Tr<T>::st4((T*)a.dstate_in + (s * (K - 1) + j) * a.C + c0, ds[j]);
+    }
+}
+
+// dweight [C, K] and dbias [C] from the workgroups' sums, in a fixed order:
+// 16 lanes a column take every 16th workgroup, then their sums are added.
+template <int K>
+__global__ __launch_bounds__(1024) void conv_backward_sum_kernel(ConvBwdArgs a, int64_t n) {
+    __shared__ float s_s[16][64];
+    const int l = threadIdx.x & 63, strip = threadIdx.x >> 6, c = blockIdx.x * 64 + l, k = blockIdx.y;
+    float s = 0.f;
+    if (c < a.C)
+        for (int64_t t = strip; t < n; t += 16) s += a.part[(t * (K + 1) + k) * a.C + c];
+    s_s[strip][l] = s;
+    __syncthreads();
+    if (strip || c >= a.C) return;
+    for (int j = 1; j < 16; ++j) s += s_s[j][l];
+    if (k < K) a.dweight[(int64_t)c * K + k] = s;
+    else if (a.dbias) a.dbias[c] = s;
+}
+
+template <typename T, typename Y, int K, bool SILU>
+hipError_t run_conv_backward(const ConvBwdArgs& a, hipStream_t stream) {
+    hipError_t e;
+    if (a.T > 0) {
+        hipLaunchKernelGGL((conv_backward_kernel<T, Y, K, SILU>),
+                           dim3((unsigned)a.nblocks, (unsigned)((a.C + kWaveCh - 1) / kWaveCh)), dim3(kBwdThreads), 0,
+                           stream, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((conv_backward_sum_kernel<K>), dim3((unsigned)((a.C + 63) / 64), K + 1), dim3(1024), 0, stream, a,
+                       (int64_t)(a.T > 0 ? a.nblocks : 0));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.dstate_in && a.nseq > 0) {
+        const int64_t n = a.nseq * (a.C / kCh);
+        hipLaunchKernelGGL((conv_backward_state_kernel<T, Y, K, SILU>),
+                           dim3((unsigned)((n + kBwdThreads - 1) / kBwdThreads)), dim3(kBwdThreads), 0, stream, a);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+template <typename T, typename Y>
+hipError_t by_width(const ConvBwdArgs& a, hipStream_t stream) {
+    switch (a.K) {
+        case 2: return a.silu ? run_conv_backward<T, Y, 2, true>(a, stream) : run_conv_backward<T, Y, 2, false>(a, stream);
+        case 3: return a.silu ? run_conv_backward<T, Y, 3, true>(a, stream) : run_conv_backward<T, Y, 3, false>(a, stream);
+        case 4: return a.silu ? run_conv_backward<T, Y, 4, true>(a, stream) : run_conv_backward<T, Y, 4, false>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+// Rows of a workgroup: 512 for long batches, fewer (in steps of 32, one batch
+// a wave) where that leaves the chip short of 1024 workgroups.
+void conv_backward_blocks(int64_t T, int32_t C, int32_t* nblocks, int32_t* block_rows) {
+    const int64_t cb = (C + kWaveCh - 1) / kWaveCh;
+    int64_t rows = T * cb / 1024 / 32 * 32;
+    rows = std::max<int64_t>(32, std::min<int64_t>(512, rows));
+    *block_rows = (int32_t)rows;
+    *nblocks = (int32_t)std::max<int64_t>(1, (T + rows - 1) / rows);
+}
+
+hipError_t launch_conv1d_backward(const ConvBwdArgs& a, hipStream_t stream) {
+    if (a.dtype == 1) return a.y_f32 ? by_width<bf16_t, float>(a, stream) : by_width<bf16_t, bf16_t>(a, stream);
+    return a.y_f32 ? by_width<float, float>(a, stream) : by_width<float, bf16_t>(a, stream);
+}
+
+}  // namespace ssd

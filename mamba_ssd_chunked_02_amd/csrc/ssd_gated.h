@@ -1,0 +1,84 @@
+// Shared by the gated recurrence's kernels: the sequence boundaries inside a
+// run of rows, and the gates of one element.
+#pragma once
+
+#include "ssd_device.h"
+
+namespace ssd {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------- rows
+// Offsets are clamped into [0, T] with the end no earlier than the start, so
+// no row or state index derived from them leaves its array, whatever the
+// device list holds.
+struct RowRange {
+    int64_t lo, hi;
+};
+
+__device__ inline RowRange seq_range(const int32_t* cu, int64_t L, int64_t T, int64_t s) {
+    if (!cu) return {s * L, s * L + L};
+    const int64_t lo = min(max((int64_t)cu[s], (int64_t)0), T);
+    return {lo, min(max((int64_t)cu[s + 1], lo), T)};
+}
+
+// Rows that belong to sequences.  Rows outside (behind the last sequence) are
+// neither read into a result nor written.
+__device__ inline RowRange live_rows(const int32_t* cu, int64_t nseq, int64_t T) {
+    if (!cu) return {0, T};
+    const int64_t lo = min(max((int64_t)cu[0], (int64_t)0), T);
+    return {lo, min(max((int64_t)cu[nseq], lo), T)};
+}
+
+// The sequence holding a live row: the last one that starts at or before it.
+__device__ inline int64_t seq_of(const int32_t* cu, int64_t nseq, int64_t L, int64_t row) {
+    if (!cu) return row / L;
+    int64_t lo = 0, hi = nseq - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= row) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------- gates
+// sigmoid with the hardware exponential and reciprocal (1 ulp each).
+__device__ inline float sigmoid_f(float v) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
+}
+
+// log(1 + exp(v)) in fp32 without cancellation on either side.
+__device__ inline float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+// The factor of sigmoid(r) in log a: -rate softplus(lam), no lower than -1e4
+// (exp of which is 0) so that sums of it stay finite; NaN stays NaN.
+__device__ inline float decay_factor(float lam, float rate) {
+    const float k = -rate * softplus_f(lam);
+    return k < -1e4f ? -1e4f : k;
+}
+
+// a = exp(v) for v <= 0, held so that neither a nor a - 1 loses digits: above
+// -0.35 as a - 1 (<= 0), from its Taylor polynomial to v^7 (the first term
+// left out is below 2^-25 of it); elsewhere as a itself (> 0), from the
+// hardware exponential.  The floor keeps the two apart where a underflows.
+__device__ inline float held_decay(float v) {
+    float p = 1.f / 5040.f;
+    p = __builtin_fmaf(p, v, 1.f / 720.f);
+    p = __builtin_fmaf(p, v, 1.f / 120.f);
+    p = __builtin_fmaf(p, v, 1.f / 24.f);
+    p = __builtin_fmaf(p, v, 1.f / 6.f);
+    p = __builtin_fmaf(p, v, 0.5f);
+    p = __builtin_fmaf(p * v, v, v);
+    const float q = fmaxf(__builtin_amdgcn_exp2f(v * 1.44269504088896341f), 1e-37f);
+    return v < -0.35f ? q : p;
+}
+__device__ inline float decay_of(float w) { return w > 0.f ? w : 1.f + w; }
+
+// 1 - a^2 = -e (2 + e) with e = a - 1: no cancellation however near a is to 1.
+__device__ inline float one_minus_a2(float w) {
+    const float e = w > 0.f ? w - 1.f : w;
+    return -e * (2.f + e);
+}
+
+}  // namespace ssd

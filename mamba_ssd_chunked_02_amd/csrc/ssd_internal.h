@@ -182,6 +182,117 @@ struct ConvArgs {
     int32_t dtype, y_f32, silu;
 };
 
+// Gated linear recurrence (ssd_gated.hip): the tokens of the whole batch are
+// cut into tiles of this many rows.
+constexpr int kGatedTileRows = 128;
+
+struct GatedArgs {
+    const void* x;             // [rows, C] with row stride x_stride (elements)
+    const void* r;
+    const void* i;
+    int64_t x_stride, r_stride, i_stride;
+    const float* lam;          // [C]
+    const float* init;         // [nseq, C] or NULL (zero)
+    const int32_t* cu;         // device [nseq+1] or NULL (dense)
+    const uint32_t* bits;      // packed: sequence boundaries, one word per run of rows
+    int64_t nseq, L, T;        // sequences, dense length, total rows
+    int32_t C;
+    int32_t dtype, y_f32;      // y_f32: y, or dy, is fp32
+    float rate;
+    void* y;                   // [rows, C]
+    float* final_state;        // [nseq, C] or NULL
+    float* states_out;         // [ntiles, C] or NULL: the state entering every tile
+    // backward
+    const void* dy;            // [rows, C]
+    const float* states_in;    // states_out of the forward pass
+    const float* dfinal;       // [nseq, C] or NULL (zero)
+    void* dx;                  // [rows, C] with row strides of their own
+    void* dr;
+    void* di;
+    int64_t dx_stride, dr_stride, di_stride;
+    float* dlam;               // [C]
+    float* dinit;              // [nseq, C] or NULL
+};
+
+// Byte offsets of the workspace regions (256-byte aligned).
+struct GatedLayout {
+    int64_t ntiles;
+    size_t bits;   // u32 per run of rows (packed)
+    size_t agg;    // f32 x2 [ntiles][C]: every tile's map of the state
+    size_t carry;  // f32 [ntiles][C]: the state (backward: adjoint) entering every tile
+    size_t dlam;   // f32 [ntiles][C]: the tiles' sums of dlam
+    size_t total;
+};
+
+GatedLayout gated_layout(int64_t T, int32_t C, bool packed, bool backward, bool keep_states);
+hipError_t launch_gated_scan(const GatedArgs& a, const GatedLayout& lay, void* ws, hipStream_t stream);
+hipError_t launch_gated_backward(const GatedArgs& a, const GatedLayout& lay, void* ws, hipStream_t stream);
+hipError_t launch_gated_step(const GatedArgs& a, const float* state, float* state_out, hipStream_t stream);
+
+// RMS norms (ssd_norm.hip).  A segment is one row's part that shares a norm
+// (the whole row, or one of its groups).
+struct NormArgs {
+    int64_t rows;
+    int32_t D, G;              // columns, groups
+    float eps;
+    int32_t a_f32, b_f32;      // types of the two inputs (see the launchers)
+    int64_t x_stride, z_stride, dx_stride, dz_stride;  // row strides, elements
+    const void* x;             // [rows, D]
+    const void* z;             // residual norm: the residual; gated norm: the gate's input
+    const float* weight;       // [D]
+    const float* scale;        // residual norm: [D] or NULL
+    int32_t norm_first;        // gated norm: the gate multiplies the normalised row
+    void* y;                   // [rows, D]
+    void* out;                 // residual norm: the new residual [rows, D]
+    float* rstd;               // [rows, G] or NULL
+    // backward
+    const void* dy;
+    const void* dout;          // residual norm: gradient of the new residual, or NULL
+    const float* rstd_in;
+    void* dx;
+    void* dz;                  // residual norm: gradient of the residual
+    float* dweight;            // [D]
+    float* dscale;             // [D] or NULL
+    float* part;               // workspace
+    int32_t nparts;            // workgroups along the rows, each with its own partial sums
+};
+
+// Largest number of columns sharing one norm.
+constexpr int32_t kMaxNormColumns = 16384;
+// Workgroups along the rows of the backward pass.
+int32_t norm_parts(int64_t rows, int32_t D, int32_t G);
+hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_residual_norm_backward(const NormArgs& a, hipStream_t stream);
+hipError_t launch_gated_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_gated_norm_backward(const NormArgs& a, hipStream_t stream);
+
+// Gradients of the conv1d (ssd_conv_bwd.hip).
+struct ConvBwdArgs {
+    const void* x;             // [rows, C]
+    const float* weight;       // [C, K]
+    const float* bias;         // [C] or NULL
+    const void* state_in;      // [nseq, K-1, C] or NULL
+    const int32_t* cu;         // device [nseq+1] or NULL (dense)
+    const void* dy[3];         // gradients of the output parts [rows, part_ch[p]]
+    int32_t part_ch[3];
+    int32_t nparts;
+    const void* dstate_out;    // gradient of the final conv state [nseq, K-1, C] or NULL
+    int64_t nseq, L, T;
+    int32_t C, K;
+    int32_t dtype, y_f32, silu;
+    void* dx;                  // [rows, C]
+    float* dweight;            // [C, K]
+    float* dbias;              // [C] or NULL
+    void* dstate_in;           // [nseq, K-1, C] or NULL
+    float* part;               // workspace [nblocks][K+1][C]
+    int32_t nblocks, block_rows;  // workgroups along the rows, rows of each
+};
+void conv_backward_blocks(int64_t T, int32_t C, int32_t* nblocks, int32_t* block_rows);
+hipError_t launch_conv1d_backward(const ConvBwdArgs& a, hipStream_t stream);
+
+// out[c] = sum over n of part[n * ld + c], in a fixed order (ssd_norm.hip).
+hipError_t launch_column_sum(const float* part, int64_t n, int64_t ld, int32_t cols, float* out, hipStream_t stream);
+
 // Sets the sentence ssd_last_error_detail() returns on this thread (for
 // entry points outside ssd_api.cpp); returns st.
 int32_t set_error_detail(int32_t st, const char* fmt, ...);
