@@ -216,6 +216,9 @@ ssd_status gated_shape_of(const ssd_gated_shape* sh, bool step, ssd::GatedArgs* 
     a->dtype = sh->dtype;
     a->y_f32 = sh->ydtype == SSD_F32;
     a->rate = sh->rate;
+    // a launch counts its lanes in 32 bits
+    if (!step && ssd::gated_layout(a->T, a->C, false, false).blocks > ((int64_t)1 << 22))
+        FAIL(SSD_ERR_SHAPE, "tensor too large for one launch");
     return SSD_OK;
 }
 
@@ -227,7 +230,7 @@ SSD_API ssd_status ssd_gated_scan_workspace_size(const ssd_gated_shape* shape, i
     ssd::GatedArgs a;
     const ssd_status st = gated_shape_of(shape, false, &a);
     if (st != SSD_OK) return st;
-    *bytes = ssd::gated_layout(a.T, a.C, a.cu != nullptr, backward, false).total;
+    *bytes = ssd::gated_layout(a.T, a.C, a.cu != nullptr, backward).total;
     return ok();
 }
 
@@ -249,7 +252,7 @@ SSD_API ssd_status ssd_gated_scan(const void* x, const void* r, const void* i, c
                         {states, "states", false, true}};
     st = check_args(args, (int)(sizeof(args) / sizeof(args[0])));
     if (st != SSD_OK) return st;
-    const ssd::GatedLayout lay = ssd::gated_layout(a.T, a.C, a.cu != nullptr, false, false);
+    const ssd::GatedLayout lay = ssd::gated_layout(a.T, a.C, a.cu != nullptr, false);
     st = check_workspace(workspace, workspace_bytes, lay.total);
     if (st != SSD_OK) return st;
     a.x = x;
@@ -287,7 +290,7 @@ SSD_API ssd_status ssd_gated_scan_backward(const void* dy, const float* dfinal_s
                         {dinit_state, "dinit_state", false, true}};
     st = check_args(args, (int)(sizeof(args) / sizeof(args[0])));
     if (st != SSD_OK) return st;
-    const ssd::GatedLayout lay = ssd::gated_layout(a.T, a.C, a.cu != nullptr, true, true);
+    const ssd::GatedLayout lay = ssd::gated_layout(a.T, a.C, a.cu != nullptr, true);
     st = check_workspace(workspace, workspace_bytes, lay.total);
     if (st != SSD_OK) return st;
     a.x = x;

@@ -58,27 +58,39 @@ __device__ inline float decay_factor(float lam, float rate) {
     return k < -1e4f ? -1e4f : k;
 }
 
-// a = exp(v) for v <= 0, held so that neither a nor a - 1 loses digits: above
-// -0.35 as a - 1 (<= 0), from its Taylor polynomial to v^7 (the first term
-// left out is below 2^-25 of it); elsewhere as a itself (> 0), from the
-// hardware exponential.  The floor keeps the two apart where a underflows.
-__device__ inline float held_decay(float v) {
-    float p = 1.f / 5040.f;
-    p = __builtin_fmaf(p, v, 1.f / 720.f);
-    p = __builtin_fmaf(p, v, 1.f / 120.f);
-    p = __builtin_fmaf(p, v, 1.f / 24.f);
-    p = __builtin_fmaf(p, v, 1.f / 6.f);
-    p = __builtin_fmaf(p, v, 0.5f);
-    p = __builtin_fmaf(p * v, v, v);
-    const float q = fmaxf(__builtin_amdgcn_exp2f(v * 1.44269504088896341f), 1e-37f);
-    return v < -0.35f ? q : p;
+// exp(v) - 1 for v in [-0.35, 0]: v times the minimax polynomial of degree 4 of
+// (exp(v) - 1) / v there, fitted by exchange on its relative error (0.22 of
+// 2^-24); 2 of 2^-24 with the roundings.
+constexpr float kSlowDecay = -0.35f;
+__device__ inline float expm1_slow(float v) {
+    float p = 0x1.d82f32p-8f;
+    p = __builtin_fmaf(p, v, 0x1.528df0p-5f);
+    p = __builtin_fmaf(p, v, 0x1.553f22p-3f);
+    p = __builtin_fmaf(p, v, 0x1.ffff82p-2f);
+    p = __builtin_fmaf(p, v, 1.f);
+    return p * v;
 }
-__device__ inline float decay_of(float w) { return w > 0.f ? w : 1.f + w; }
 
-// 1 - a^2 = -e (2 + e) with e = a - 1: no cancellation however near a is to 1.
+// a = exp(v) and m = 1 - a^2 of one element, from the held decay w: a - 1 (<= 0)
+// where v >= -0.35, elsewhere a itself (> 0), so that neither a nor a - 1 loses
+// digits.  m = -e (1 + a) with e = a - 1 has no cancellation however near a is
+// to 1.  SLOW: every channel of the wave decays by no more than 0.35 a token, so
+// that no element takes the exponential.
+template <bool SLOW>
+__device__ inline float held_decay(float v) {
+    if constexpr (SLOW) return expm1_slow(v);
+    // the floor keeps w > 0 where a underflows
+    const float q = fmaxf(__builtin_amdgcn_exp2f(v * 1.44269504088896341f), 1e-37f);
+    return v < kSlowDecay ? q : expm1_slow(v);
+}
+template <bool SLOW>
+__device__ inline float decay_of(float w) {
+    return !SLOW && w > 0.f ? w : 1.f + w;
+}
+template <bool SLOW>
 __device__ inline float one_minus_a2(float w) {
-    const float e = w > 0.f ? w - 1.f : w;
-    return -e * (2.f + e);
+    const float e = !SLOW && w > 0.f ? w - 1.f : w;
+    return __builtin_fmaf(-e, decay_of<SLOW>(w), -e);
 }
 
 }  // namespace ssd

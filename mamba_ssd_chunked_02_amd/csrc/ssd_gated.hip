@@ -2,8 +2,8 @@
 // computed from two logits of every token,
 //   log a_t = -rate softplus(lam) sigmoid(r_t)
 //   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t,
-// and its gradients.  A few dozen fp32 operations and 8 bytes (bf16) an
-// element: an HBM stream, with the vector ALU close behind.
+// and its gradients.  About 40 fp32 operations (6 of them quarter rate) and 8
+// bytes (bf16) an element: an HBM stream, with the vector ALU close behind.
 //
 // The token axis of the whole batch is cut into tiles of kTileRows rows
 // whatever the sequences' lengths; a sequence start inside a tile resets the
@@ -13,11 +13,23 @@
 // otherwise), so that nothing of the earlier sequence, NaN and infinities
 // included, gets through a multiplication by 0.
 //
+// One pass over the data: a workgroup holds its tile in registers, publishes
+// the tile's map, folds the maps of the tiles before it into the state that
+// enters its own, and finishes.  Tiles go in groups of 16: a tile folds the maps
+// of its group's earlier tiles, in order, onto the state entering the group,
+// which the last tile of the group before publishes.  So the order of every sum
+// is fixed, and only one step in 16 tiles is a chain.
+//   Why the waits end: the tiles of a channel block are handed out in order by
+// a counter, so every tile that a workgroup waits for belongs to a workgroup
+// that runs already, and a tile's map is published before its workgroup waits
+// for anything.  The state entering a group waits only for earlier tiles.
+//
 // A decay near 1 is rounded to fp32 once (half of 2^-24); the factor P of a run
 // comes from the sum of its log a, so these roundings do not add up from run
 // to run over a memory of thousands of tokens.  1 - a^2 comes from a - 1, which
 // is computed by itself.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssd_gated.h"
 
@@ -28,45 +40,65 @@ namespace {
 constexpr int kLaneCh = 4;                      // channels per lane
 constexpr int kSegLanes = 16;                   // lanes across the channels of a row
 constexpr int kTileCh = kLaneCh * kSegLanes;    // channels per workgroup
-constexpr int kSegs = 16;                       // runs of rows per tile, one per 16 lanes
-constexpr int kSegRows = 8;                     // rows per run
 constexpr int kTileRows = kGatedTileRows;
-static_assert(kSegs * kSegRows == kTileRows, "a tile is kSegs runs");
-constexpr int kThreads = kSegs * kSegLanes;
+constexpr int kGroup = 16;                      // tiles per group of the carry
+constexpr int kBitRows = 8;                     // rows per word of boundary bits
+constexpr int kFwdRows = 8, kBwdRows = 4;       // rows per run (per lane)
+constexpr uint64_t kNotYet = ~(uint64_t)0;      // a published word that is not there yet
 
 __device__ inline bool is_reset(float P) { return __builtin_bit_cast(int, P) < 0; }
 
-// The run after (P, H): applied to a state.
+// The run (P, H) applied to a state.
 __device__ inline float advance(float P, float H, float h) { return is_reset(P) ? H : __builtin_fmaf(P, h, H); }
+// The factor of a run followed by one with factor P.
+__device__ inline float chain(float before, float P) { return is_reset(P) ? -1.f : before * P; }
 
 __device__ inline float nan_to_positive(float P) {
     return P != P ? __builtin_bit_cast(float, 0x7fc00000) : P;
 }
 
-// Boundary bits of the kSegRows rows from t0: bit j: row t0 + j is its
-// sequence's first one; bit 16 + j: its last one.
+// A pair of floats as one word that is stored and loaded whole, past the
+// caches of one XCD.  hi is no NaN with its sign bit set, so never kNotYet.
+__device__ inline void publish(uint64_t* p, float hi, float lo) {
+    const uint64_t v = (uint64_t)__builtin_bit_cast(uint32_t, hi) << 32 | __builtin_bit_cast(uint32_t, lo);
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline uint64_t look(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline bool there(uint64_t v) { return (uint32_t)(v >> 32) != 0xffffffffu; }
+__device__ inline float hi_of(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)(v >> 32)); }
+__device__ inline float lo_of(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)v); }
+
+// Boundary bits of ROWS rows from t0 (a multiple of ROWS): bit j: row t0 + j is
+// its sequence's first one; bit 16 + j: its last one.
+template <int ROWS>
 __device__ inline uint32_t boundary_bits(const GatedArgs& a, int64_t t0) {
-    uint32_t m = 0;
-    if (!a.cu) {
-        uint32_t p = (uint32_t)t0 % (uint32_t)a.L;  // rows < 2^31
-        for (int64_t j = p ? a.L - p : 0; j <= kSegRows; j += a.L) {
-            if (j < kSegRows) m |= 1u << j;
-            if (j > 0) m |= 1u << (15 + j);
-        }
-        return m;
+    if (a.cu) {
+        const uint32_t w = a.bits[t0 / kBitRows] >> (t0 % kBitRows);
+        return w & (((1u << ROWS) - 1) * 0x10001u);
     }
-    return a.bits[t0 / kSegRows];
+    uint32_t m = 0;
+    const uint32_t p = (uint32_t)t0 % (uint32_t)a.L;  // rows < 2^31
+    for (int64_t j = p ? a.L - p : 0; j <= ROWS; j += a.L) {
+        if (j < ROWS) m |= 1u << j;
+        if (j > 0) m |= 1u << (15 + j);
+    }
+    return m;
 }
 
-// Packed batches: the boundary bits of every run of rows, and the states of
-// sequences without tokens (their state passes through: out = in).
-__global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, uint32_t* bits, const float* in, float* out) {
-    const int64_t nruns = (a.T + kSegRows - 1) / kSegRows;
+// Before the pass: the published words set to kNotYet and the counters to 0;
+// for a packed batch the boundary bits, and the states of sequences without
+// tokens (their state passes through: out = in).
+__global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, GatedPlan pl) {
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     const int64_t me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    for (int64_t k = me; k < pl.nwords; k += stride) pl.words[k] = kNotYet;
+    for (int64_t k = me; k < pl.ncounters; k += stride) pl.counters[k] = 0;
+    const int64_t nruns = (a.T + kBitRows - 1) / kBitRows;
     const RowRange live = live_rows(a.cu, a.nseq, a.T);
-    for (int64_t k = me; bits && k < nruns; k += stride) {
-        const int64_t t0 = k * kSegRows, t1 = min(t0 + kSegRows, live.hi);
+    for (int64_t k = me; pl.bits && k < nruns; k += stride) {
+        const int64_t t0 = k * kBitRows, t1 = min(t0 + kBitRows, live.hi);
         uint32_t m = 0;
         // every offset in [t0, t1] ends a sequence at the row before it and starts one at its row
         for (int64_t t = max(t0, live.lo); t <= t1;) {
@@ -82,19 +114,20 @@ __global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, uint32_t* 
             if (at > t0) m |= 1u << (15 + at - t0);
             t = at + 1;
         }
-        bits[k] = m;
+        pl.bits[k] = m;
     }
-    if (!out) return;
+    if (!pl.out) return;
     const int64_t waves = stride / 64, lane = me & 63;
     for (int64_t s = me / 64; s < a.nseq; s += waves) {
         const RowRange q = seq_range(a.cu, a.L, a.T, s);
         if (q.hi > q.lo) continue;
-        for (int64_t c = lane; c < a.C; c += 64) out[s * a.C + c] = in ? in[s * a.C + c] : 0.f;
+        for (int64_t c = lane; c < a.C; c += 64) pl.out[s * a.C + c] = pl.in ? pl.in[s * a.C + c] : 0.f;
     }
 }
 
 // What a lane has of its run of rows: the place, the boundary bits and the
 // live rows (bit j).
+template <int ROWS>
 struct Run {
     int64_t t0;
     int c0;          // first channel (clamped into the row)
@@ -103,35 +136,28 @@ struct Run {
     __device__ bool start(int j) const { return bits >> j & 1; }
     __device__ bool end(int j) const { return bits >> (16 + j) & 1; }
     __device__ bool has(int j) const { return live >> j & 1; }
+    __device__ bool any_start() const { return bits & live; }
+    __device__ bool any_end() const { return bits >> 16 & live; }
+
+    __device__ Run(const GatedArgs& a, int64_t tile, int cb) {
+        t0 = tile * kTileRows + (threadIdx.x / kSegLanes) * ROWS;
+        const int c = cb * kTileCh + (threadIdx.x % kSegLanes) * kLaneCh;
+        on = c < a.C;
+        c0 = on ? c : a.C - kLaneCh;
+        bits = t0 < a.T ? boundary_bits<ROWS>(a, t0) : 0;
+        const RowRange r = live_rows(a.cu, a.nseq, a.T);
+        const int lo = (int)min(max(r.lo - t0, (int64_t)0), (int64_t)ROWS);
+        const int hi = (int)min(max(r.hi - t0, (int64_t)lo), (int64_t)ROWS);
+        live = ((1u << hi) - 1) & ~((1u << lo) - 1);
+    }
 };
 
-__device__ inline Run this_run(const GatedArgs& a, int64_t tile, int cblock) {
-    Run u;
-    const int seg = threadIdx.x / kSegLanes;
-    u.t0 = tile * kTileRows + seg * kSegRows;
-    const int c = cblock * kTileCh + (threadIdx.x % kSegLanes) * kLaneCh;
-    u.on = c < a.C;
-    u.c0 = u.on ? c : a.C - kLaneCh;
-    u.bits = u.t0 < a.T ? boundary_bits(a, u.t0) : 0;
-    const RowRange r = live_rows(a.cu, a.nseq, a.T);
-    const int lo = (int)min(max(r.lo - u.t0, (int64_t)0), (int64_t)kSegRows);
-    const int hi = (int)min(max(r.hi - u.t0, (int64_t)lo), (int64_t)kSegRows);
-    u.live = ((1u << hi) - 1) & ~((1u << lo) - 1);
-    return u;
-}
-
-template <typename T>
-__device__ inline void load_rows(const GatedArgs& a, const Run& u, const void* p, int64_t stride,
-                                 typename Tr<T>::v4 (&v)[kSegRows]) {
+template <typename T, int ROWS>
+__device__ inline void load_rows(const GatedArgs& a, const Run<ROWS>& u, const void* p, int64_t stride,
+                                 typename Tr<T>::v4 (&v)[ROWS]) {
 #pragma unroll
-    for (int j = 0; j < kSegRows; ++j)
+    for (int j = 0; j < ROWS; ++j)
         v[j] = Tr<T>::ld4raw((const T*)p + min(u.t0 + j, a.T - 1) * stride + u.c0);
-}
-
-// The factor of sigmoid(r) for the workgroup's channels, in LDS.
-__device__ inline void load_factors(const GatedArgs& a, int cblock, float* k) {
-    if (threadIdx.x < kTileCh)
-        k[threadIdx.x] = decay_factor(a.lam[min(cblock * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
 }
 
 __device__ inline f32x4 seq_state(const float* st, const GatedArgs& a, int64_t row, int c0) {
@@ -139,7 +165,7 @@ __device__ inline f32x4 seq_state(const float* st, const GatedArgs& a, int64_t r
 }
 
 // log a, the held decay and b of one row's four channels.
-template <typename T>
+template <typename T, bool SLOW>
 struct Step {
     f32x4 loga, w, b;
     __device__ Step(f32x4 k, typename Tr<T>::v4 xv, typename Tr<T>::v4 rv, typename Tr<T>::v4 iv) {
@@ -147,105 +173,176 @@ struct Step {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             loga[c] = k[c] * sigmoid_f(r[c]);
-            w[c] = held_decay(loga[c]);
-            b[c] = __builtin_amdgcn_sqrtf(one_minus_a2(w[c])) * sigmoid_f(i[c]) * x[c];
+            w[c] = held_decay<SLOW>(loga[c]);
+            b[c] = __builtin_amdgcn_sqrtf(one_minus_a2<SLOW>(w[c])) * sigmoid_f(i[c]) * x[c];
         }
     }
-    __device__ f32x4 a() const { return decay4(w); }
-    __device__ static f32x4 decay4(f32x4 w) {
-        return f32x4{decay_of(w[0]), decay_of(w[1]), decay_of(w[2]), decay_of(w[3])};
+};
+template <bool SLOW>
+__device__ inline f32x4 decay4(f32x4 w) {
+    return f32x4{decay_of<SLOW>(w[0]), decay_of<SLOW>(w[1]), decay_of<SLOW>(w[2]), decay_of<SLOW>(w[3])};
+}
+
+// A run's factor from its sum of log a.
+__device__ inline f32x4 run_factor(f32x4 S, bool reset) {
+    f32x4 P;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        P[c] = reset ? -1.f : nan_to_positive(__builtin_amdgcn_exp2f(S[c] * 1.44269504088896341f));
+    return P;
+}
+
+// Which tile this workgroup has: the channel block's next one, in the pass's
+// order.
+__device__ inline int64_t next_tile(const GatedPass& ps, int cb, uint32_t* slot) {
+    if (!ps.counters) return 0;
+    if (threadIdx.x == 0) *slot = atomicAdd(ps.counters + cb * kGatedCounterStride, 1u);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*slot);
+}
+
+// The runs' maps in LDS, folded in order (REV: from the last run back).
+template <int RUNS, bool REV>
+struct Fold {
+    const float *P, *H;  // [RUNS][kTileCh]
+    __device__ static int at(int s) { return (REV ? RUNS - 1 - s : s) * kTileCh; }
+    // the tile's own map
+    __device__ void map(int ch, float& Pt, float& Ht) const {
+        Pt = 1.f;
+        Ht = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < RUNS; ++s) {
+            const float p = P[at(s) + ch];
+            Ht = advance(p, H[at(s) + ch], Ht);
+            Pt = chain(Pt, p);
+        }
+    }
+    // H replaced by the state entering each run
+    __device__ void enter(int ch, float h) const {
+#pragma unroll 8
+        for (int s = 0; s < RUNS; ++s) {
+            float* const to = const_cast<float*>(H) + at(s) + ch;
+            const float n = advance(P[at(s) + ch], *to, h);
+            *to = h;
+            h = n;
+        }
     }
 };
 
+// The state entering tile `ord` (counted in the pass's order) for channel
+// ch of the workgroup, valid in wave 0.  (Pt, Ht): the tile's own map, in wave 0.
+// Every wave calls it; group_s: [kGroup][kTileCh] pairs.
+template <int WAVES>
+__device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, int C, float Pt, float Ht, f32x2* group_s) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const bool on = chan < C;
+    const int p = (int)(ord % kGroup);
+    const int64_t g = ord / kGroup;
+    if (wave == 0 && on && p < kGroup - 1 && ord + 1 < ps.ntiles) publish(ps.maps + ord * C + chan, Pt, Ht);
+    // the maps of the group's earlier tiles: wave w takes kGroup / WAVES of them
+    constexpr int kEach = kGroup / WAVES;
+    uint64_t v[kEach];
+    const int j0 = wave * kEach;
+    if (j0 < p) {
+        const uint64_t* m = ps.maps + (g * kGroup + j0) * C + (on ? chan : 0);
+        while (true) {
+            bool ready = true;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                v[j] = j0 + j < p ? look(m + (int64_t)j * C) : 0;
+                ready &= there(v[j]);
+            }
+            if (__all(ready)) break;
+            __builtin_amdgcn_s_sleep(1);
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) group_s[(j0 + j) * kTileCh + lane] = f32x2{hi_of(v[j]), lo_of(v[j])};
+    }
+    __syncthreads();
+    if (wave) return 0.f;
+    float Pp = 1.f, h = 0.f;
+    for (int j = 0; j < p; ++j) {
+        const f32x2 m = group_s[j * kTileCh + lane];
+        h = advance(m[0], m[1], h);
+        Pp = chain(Pp, m[0]);
+    }
+    if (g > 0 && !__all(is_reset(Pp))) {
+        const uint64_t* c = ps.entry + g * C + (on ? chan : 0);
+        uint64_t e;
+        while (true) {
+            e = look(c);
+            if (__all(there(e))) break;
+            __builtin_amdgcn_s_sleep(1);
+        }
+        h = advance(Pp, h, lo_of(e));
+    }
+    if (on && p == kGroup - 1 && ord + 1 < ps.ntiles) publish(ps.entry + (g + 1) * C + chan, 0.f, advance(Pt, Ht, h));
+    return h;
+}
+
 // ------------------------------------------------------------------ forward
-// The forward pass of one tile: with AGG only its map (P, H) per channel is
-// written; otherwise the state entering the tile is read and y is written.
-template <typename T, typename Y, bool AGG>
-__global__ __launch_bounds__(kThreads) void gated_forward_kernel(GatedArgs a, f32x2* agg, const float* states) {
+template <typename T, typename Y>
+__global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forward_kernel(GatedArgs a, GatedPass ps) {
+    constexpr int R = kFwdRows, kRuns = kTileRows / R;
+    __shared__ uint32_t slot;
     __shared__ float k_s[kTileCh];
-    __shared__ f32x4 P_s[kSegs][kSegLanes], H_s[kSegs][kSegLanes];
+    __shared__ f32x4 P_s[kRuns][kSegLanes], H_s[kRuns][kSegLanes];
+    __shared__ f32x2 group_s[kGroup * kTileCh];
     const int seg = threadIdx.x / kSegLanes, ln = threadIdx.x % kSegLanes;
-    const int64_t tile = blockIdx.x;
-    const int cb = blockIdx.y;
-    const Run u = this_run(a, tile, cb);
-    load_factors(a, cb, k_s);
-    typename Tr<T>::v4 xv[kSegRows], rv[kSegRows], iv[kSegRows];
+    const int cb = blockIdx.x % ps.nblocks;
+    if (threadIdx.x < kTileCh)
+        k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
+    const int64_t tile = next_tile(ps, cb, &slot);
+    const Run<R> u(a, tile, cb);
+    typename Tr<T>::v4 xv[R], rv[R], iv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
     load_rows<T>(a, u, a.i, a.i_stride, iv);
     load_rows<T>(a, u, a.x, a.x_stride, xv);
     __syncthreads();
     const f32x4 k = *(const f32x4*)(k_s + ln * kLaneCh);
 
-    f32x4 av[kSegRows], b[kSegRows], S = {}, H = {};
-    bool reset = false;
+    f32x4 av[R], b[R], S = {}, H = {};
+    auto local = [&](auto slow) {
+        constexpr bool SLOW = decltype(slow)::value;
 #pragma unroll
-    for (int j = 0; j < kSegRows; ++j) {
-        const Step<T> st(k, xv[j], rv[j], iv[j]);
-        av[j] = st.a();
-        b[j] = st.b;
-        if (u.has(j)) {
-            if (u.start(j)) {
-                H = seq_state(a.init, a, u.t0 + j, u.c0);
-                reset = true;
+        for (int j = 0; j < R; ++j) {
+            const Step<T, SLOW> st(k, xv[j], rv[j], iv[j]);
+            av[j] = decay4<SLOW>(st.w);
+            b[j] = st.b;
+            if (u.has(j)) {
+                if (u.start(j)) H = seq_state(a.init, a, u.t0 + j, u.c0);
+                S += st.loga;
+                H = av[j] * H + b[j];
             }
-            S += st.loga;
-            H = av[j] * H + b[j];
         }
-    }
-    f32x4 P;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) P[c] = reset ? -1.f : nan_to_positive(__builtin_amdgcn_exp2f(S[c] * 1.44269504f));
-    P_s[seg][ln] = P;
+    };
+    if (__any(fminf(fminf(k[0], k[1]), fminf(k[2], k[3])) < kSlowDecay)) local(std::false_type{});
+    else local(std::true_type{});
+    P_s[seg][ln] = run_factor(S, u.any_start());
     H_s[seg][ln] = H;
     __syncthreads();
-    // one lane per channel folds the runs
+    const Fold<kRuns, false> fold{(const float*)P_s, (const float*)H_s};
+    const int ch = threadIdx.x & 63, chan = cb * kTileCh + ch;
+    float Pt = 1.f, Ht = 0.f, h0 = 0.f;
+    if (ps.counters) {
+        if (threadIdx.x < kTileCh) fold.map(ch, Pt, Ht);
+        h0 = enter_tile<kRuns / 4>(ps, tile, chan, a.C, Pt, Ht, group_s);
+    }
     if (threadIdx.x < kTileCh) {
-        const int l = threadIdx.x / 4, c = threadIdx.x % 4, ch = cb * kTileCh + threadIdx.x;
-        if constexpr (AGG) {
-            float Pt = 1.f, Ht = 0.f;
-            for (int s = 0; s < kSegs; ++s) {
-                const float Pk = P_s[s][l][c];
-                Ht = advance(Pk, H_s[s][l][c], Ht);
-                Pt = is_reset(Pk) ? -1.f : Pt * Pk;
-            }
-            if (ch < a.C) agg[tile * a.C + ch] = f32x2{Pt, Ht};
-        } else {
-            float h = ch < a.C ? states[tile * a.C + ch] : 0.f;
-            for (int s = 0; s < kSegs; ++s) {
-                const float n = advance(P_s[s][l][c], H_s[s][l][c], h);
-                H_s[s][l][c] = h;  // the state entering the run
-                h = n;
-            }
-        }
+        if (a.states_out && chan < a.C) a.states_out[tile * a.C + chan] = h0;
+        fold.enter(ch, h0);
     }
-    if constexpr (!AGG) {
-        __syncthreads();
-        if (!u.on) return;
-        f32x4 h = H_s[seg][ln];
+    __syncthreads();
+    if (!u.on) return;
+    f32x4 h = H_s[seg][ln];
 #pragma unroll
-        for (int j = 0; j < kSegRows; ++j) {
-            if (!u.has(j)) continue;
-            if (u.start(j)) h = seq_state(a.init, a, u.t0 + j, u.c0);
-            h = av[j] * h + b[j];
-            Tr<Y>::st4((Y*)a.y + (u.t0 + j) * a.C + u.c0, h);
-            if (a.final_state && u.end(j))
-                *(f32x4*)(a.final_state + seq_of(a.cu, a.nseq, a.L, u.t0 + j) * a.C + u.c0) = h;
-        }
-    }
-}
-
-// The state entering every tile, from the tiles' maps in order (REV: from the
-// last one back: the adjoint entering every tile from behind).
-template <bool REV>
-__global__ __launch_bounds__(64) void gated_carry_kernel(int64_t ntiles, int C, const f32x2* agg, float* states) {
-    const int ch = blockIdx.x * 64 + threadIdx.x;
-    if (ch >= C) return;
-    float h = 0.f;
-    for (int64_t t = 0; t < ntiles; ++t) {
-        const int64_t k = REV ? ntiles - 1 - t : t;
-        states[k * C + ch] = h;
-        const f32x2 m = agg[k * C + ch];
-        h = advance(m[0], m[1], h);
+    for (int j = 0; j < R; ++j) {
+        if (!u.has(j)) continue;
+        if (u.start(j)) h = seq_state(a.init, a, u.t0 + j, u.c0);
+        h = av[j] * h + b[j];
+        Tr<Y>::st4((Y*)a.y + (u.t0 + j) * a.C + u.c0, h);
+        if (a.final_state && u.end(j))
+            *(f32x4*)(a.final_state + seq_of(a.cu, a.nseq, a.L, u.t0 + j) * a.C + u.c0) = h;
     }
 }
 
@@ -256,109 +353,101 @@ __global__ __launch_bounds__(64) void gated_carry_kernel(int64_t ntiles, int C, 
 //   d log a = g (a h_{t-1} - a^2 / beta sig(i) x),
 //   dr = dloga loga (1 - sig(r)),  dlam = sum dloga loga sigmoid(lam)/softplus(lam),
 //   dinit = q at a sequence's first token.
-// h_{t-1} is recomputed in fp32 from the state entering the tile.
-template <typename T, typename Y, bool AGG>
-__global__ __launch_bounds__(kThreads) void gated_backward_kernel(GatedArgs a, f32x2* agg, const float* adjoints,
-                                                                  float* dlam_part) {
+// h_{t-1} is recomputed in fp32 from the state entering the tile, which the
+// forward pass kept; the adjoint is carried over the tiles in reverse order.
+template <typename T, typename Y>
+__global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backward_kernel(GatedArgs a, GatedPass ps,
+                                                                                          float* dlam_part) {
+    constexpr int R = kBwdRows, kRuns = kTileRows / R;
+    __shared__ uint32_t slot;
     __shared__ float k_s[kTileCh];
-    __shared__ f32x4 P_s[kSegs][kSegLanes], H_s[kSegs][kSegLanes], R_s[kSegs][kSegLanes], Q_s[kSegs][kSegLanes];
+    __shared__ f32x4 P_s[kRuns][kSegLanes], H_s[kRuns][kSegLanes], R_s[kRuns][kSegLanes], Q_s[kRuns][kSegLanes];
+    __shared__ f32x2 group_s[kGroup * kTileCh];
     const int seg = threadIdx.x / kSegLanes, ln = threadIdx.x % kSegLanes;
-    const int64_t tile = blockIdx.x;
-    const int cb = blockIdx.y;
-    const Run u = this_run(a, tile, cb);
-    load_factors(a, cb, k_s);
-    typename Tr<T>::v4 xv[kSegRows], rv[kSegRows], iv[kSegRows];
-    typename Tr<Y>::v4 dv[kSegRows];
+    const int cb = blockIdx.x % ps.nblocks;
+    if (threadIdx.x < kTileCh)
+        k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
+    const int64_t ord = next_tile(ps, cb, &slot), tile = ps.ntiles - 1 - ord;
+    const Run<R> u(a, tile, cb);
+    typename Tr<T>::v4 xv[R], rv[R], iv[R];
+    typename Tr<Y>::v4 dv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
     load_rows<Y>(a, u, a.dy, a.C, dv);
     load_rows<T>(a, u, a.i, a.i_stride, iv);
     load_rows<T>(a, u, a.x, a.x_stride, xv);
+    const int ch = threadIdx.x & 63, chan = cb * kTileCh + ch;
+    // wave 1 folds the states, wave 0 the adjoints
+    const float state0 = threadIdx.x >> 6 == 1 && chan < a.C ? a.states_in[tile * a.C + chan] : 0.f;
     __syncthreads();
     const f32x4 k = *(const f32x4*)(k_s + ln * kLaneCh);
+    const bool slow_wave = !__any(fminf(fminf(k[0], k[1]), fminf(k[2], k[3])) < kSlowDecay);
 
-    f32x4 w[kSegRows], b[kSegRows], S = {}, H = {}, Q = {};
-    bool reset = false, rreset = false;
+    f32x4 w[R], b[R], S = {}, H = {}, Q = {};
+    auto local = [&](auto slow) {
+        constexpr bool SLOW = decltype(slow)::value;
 #pragma unroll
-    for (int j = 0; j < kSegRows; ++j) {
-        const Step<T> st(k, xv[j], rv[j], iv[j]);
-        w[j] = st.w;
-        b[j] = st.b;
-        if (u.has(j)) {
-            if (u.start(j)) {
-                H = seq_state(a.init, a, u.t0 + j, u.c0);
-                reset = true;
+        for (int j = 0; j < R; ++j) {
+            const Step<T, SLOW> st(k, xv[j], rv[j], iv[j]);
+            w[j] = st.w;
+            b[j] = st.b;
+            if (u.has(j)) {
+                if (u.start(j)) H = seq_state(a.init, a, u.t0 + j, u.c0);
+                S += st.loga;
+                H = decay4<SLOW>(st.w) * H + b[j];
             }
-            rreset |= u.end(j);
-            S += st.loga;
-            H = st.a() * H + b[j];
         }
-    }
 #pragma unroll
-    for (int j = kSegRows - 1; j >= 0; --j)
-        if (u.has(j)) {
-            if (u.end(j)) Q = seq_state(a.dfinal, a, u.t0 + j, u.c0);
-            const f32x4 g = Q + Tr<Y>::widen4(dv[j]);
-            Q = Step<T>::decay4(w[j]) * g;
-        }
-    f32x4 P;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) P[c] = nan_to_positive(__builtin_amdgcn_exp2f(S[c] * 1.44269504f));
-    const f32x4 marked = {-1.f, -1.f, -1.f, -1.f};
-    P_s[seg][ln] = reset ? marked : P;
+        for (int j = R - 1; j >= 0; --j)
+            if (u.has(j)) {
+                if (u.end(j)) Q = seq_state(a.dfinal, a, u.t0 + j, u.c0);
+                Q = decay4<SLOW>(w[j]) * (Q + Tr<Y>::widen4(dv[j]));
+            }
+    };
+    if (slow_wave) local(std::true_type{});
+    else local(std::false_type{});
+    P_s[seg][ln] = run_factor(S, u.any_start());
     H_s[seg][ln] = H;
-    R_s[seg][ln] = rreset ? marked : P;
+    R_s[seg][ln] = run_factor(S, u.any_end());
     Q_s[seg][ln] = Q;
     __syncthreads();
-    if (threadIdx.x < kTileCh) {
-        const int l = threadIdx.x / 4, c = threadIdx.x % 4, ch = cb * kTileCh + threadIdx.x;
-        if constexpr (AGG) {
-            float Pt = 1.f, Qt = 0.f;
-            for (int s = kSegs - 1; s >= 0; --s) {
-                const float Pk = R_s[s][l][c];
-                Qt = advance(Pk, Q_s[s][l][c], Qt);
-                Pt = is_reset(Pk) ? -1.f : Pt * Pk;
-            }
-            if (ch < a.C) agg[tile * a.C + ch] = f32x2{Pt, Qt};
-        } else {
-            float h = ch < a.C ? a.states_in[tile * a.C + ch] : 0.f, q = ch < a.C ? adjoints[tile * a.C + ch] : 0.f;
-            for (int s = 0; s < kSegs; ++s) {
-                const float n = advance(P_s[s][l][c], H_s[s][l][c], h);
-                H_s[s][l][c] = h;
-                h = n;
-            }
-            for (int s = kSegs - 1; s >= 0; --s) {
-                const float n = advance(R_s[s][l][c], Q_s[s][l][c], q);
-                Q_s[s][l][c] = q;
-                q = n;
-            }
-        }
+    const Fold<kRuns, false> states{(const float*)P_s, (const float*)H_s};
+    const Fold<kRuns, true> adjoints{(const float*)R_s, (const float*)Q_s};
+    if (threadIdx.x >> 6 == 1) states.enter(ch, state0);
+    float Rt = 1.f, Qt = 0.f, q0 = 0.f;
+    if (ps.counters) {
+        if (threadIdx.x < kTileCh) adjoints.map(ch, Rt, Qt);
+        q0 = enter_tile<kRuns / 4>(ps, ord, chan, a.C, Rt, Qt, group_s);
     }
-    if constexpr (!AGG) {
-        __syncthreads();
-        f32x4 h = H_s[seg][ln], q = Q_s[seg][ln], before[kSegRows], dl = {};
+    if (threadIdx.x < kTileCh) adjoints.enter(ch, q0);
+    __syncthreads();
+
+    f32x4 h = H_s[seg][ln], q = Q_s[seg][ln], dl = {};
+    auto finish = [&](auto slow) {
+        constexpr bool SLOW = decltype(slow)::value;
 #pragma unroll
-        for (int j = 0; j < kSegRows; ++j)
+        for (int j = 0; j < R; ++j)
             if (u.has(j)) {
                 if (u.start(j)) h = seq_state(a.init, a, u.t0 + j, u.c0);
-                before[j] = h;
-                h = Step<T>::decay4(w[j]) * h + b[j];
+                const f32x4 n = decay4<SLOW>(w[j]) * h + b[j];
+                b[j] = h;  // from here on the state before the row
+                h = n;
             }
 #pragma unroll
-        for (int j = kSegRows - 1; j >= 0; --j) {
+        for (int j = R - 1; j >= 0; --j) {
             if (!u.has(j)) continue;
             if (u.end(j)) q = seq_state(a.dfinal, a, u.t0 + j, u.c0);
             const f32x4 g = q + Tr<Y>::widen4(dv[j]);
-            q = Step<T>::decay4(w[j]) * g;
+            q = decay4<SLOW>(w[j]) * g;
             const f32x4 x = Tr<T>::widen4(xv[j]), r = Tr<T>::widen4(rv[j]), i = Tr<T>::widen4(iv[j]);
             f32x4 dx, di, dr;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float sr = sigmoid_f(r[c]), si = sigmoid_f(i[c]);
+                const float sr = sigmoid_f(r[c]), si = sigmoid_f(i[c]), av = decay_of<SLOW>(w[j][c]);
                 // 1 - a^2 = 0 only where log a is 0, and its square root's reciprocal meets that factor below;
                 // a floor (the least normal number) keeps their product 0 (a NaN passes)
-                const float m0 = one_minus_a2(w[j][c]), m = m0 < 0x1p-126f ? 0x1p-126f : m0;
-                const float rb = __builtin_amdgcn_rsqf(m), beta = m0 * rb, av = decay_of(w[j][c]);
-                const float dl0 = g[c] * av * (before[j][c] - av * rb * si * x[c]) * (k[c] * sr);
+                const float m0 = one_minus_a2<SLOW>(w[j][c]), m = m0 < 0x1p-126f ? 0x1p-126f : m0;
+                const float rb = __builtin_amdgcn_rsqf(m), beta = m0 * rb;
+                const float dl0 = g[c] * av * (b[j][c] - av * rb * si * x[c]) * (k[c] * sr);
                 dx[c] = g[c] * beta * si;
                 di[c] = dx[c] * x[c] * (1.f - si);
                 dr[c] = dl0 * (1.f - sr);
@@ -371,15 +460,17 @@ __global__ __launch_bounds__(kThreads) void gated_backward_kernel(GatedArgs a, f
             if (a.dinit && u.start(j))
                 *(f32x4*)(a.dinit + seq_of(a.cu, a.nseq, a.L, u.t0 + j) * a.C + u.c0) = q;
         }
-        __syncthreads();
-        H_s[seg][ln] = dl;
-        __syncthreads();
-        if (threadIdx.x < kTileCh) {
-            const int l = threadIdx.x / 4, c = threadIdx.x % 4, ch = cb * kTileCh + threadIdx.x;
-            float s = 0.f;
-            for (int j = 0; j < kSegs; ++j) s += H_s[j][l][c];
-            if (ch < a.C) dlam_part[tile * a.C + ch] = s;
-        }
+    };
+    if (slow_wave) finish(std::true_type{});
+    else finish(std::false_type{});
+    __syncthreads();
+    P_s[seg][ln] = dl;
+    __syncthreads();
+    if (threadIdx.x < kTileCh) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int j = 0; j < kRuns; ++j) s += ((const float*)P_s)[j * kTileCh + ch];
+        if (chan < a.C) dlam_part[tile * a.C + chan] = s;
     }
 }
 
@@ -409,65 +500,60 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a, const floa
     const int64_t n = id / quads;
     const int c0 = (int)(id - n * quads) * kLaneCh;
     f32x4 h = *(const f32x4*)(state + n * a.C + c0), k = *(const f32x4*)(a.lam + c0);
-    const Step<T> st((f32x4){decay_factor(k[0], a.rate), decay_factor(k[1], a.rate), decay_factor(k[2], a.rate),
+    const Step<T, false> st((f32x4){decay_factor(k[0], a.rate), decay_factor(k[1], a.rate), decay_factor(k[2], a.rate),
                              decay_factor(k[3], a.rate)},
                      Tr<T>::ld4raw((const T*)a.x + n * a.x_stride + c0),
                      Tr<T>::ld4raw((const T*)a.r + n * a.r_stride + c0),
                      Tr<T>::ld4raw((const T*)a.i + n * a.i_stride + c0));
-    h = st.a() * h + st.b;
+    h = decay4<false>(st.w) * h + st.b;
     *(f32x4*)(state_out + n * a.C + c0) = h;
     Tr<Y>::st4((Y*)a.y + n * a.C + c0, h);
 }
 
 inline unsigned blocks_of(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
 
-// The plan: boundary bits of a packed batch and the states of empty sequences.
-hipError_t run_plan(const GatedArgs& a, uint32_t* bits, const float* in, float* out, hipStream_t stream) {
-    if (!a.cu && a.T > 0) return hipSuccess;
-    if (!bits && !out) return hipSuccess;
-    const int64_t items = (a.T + kSegRows - 1) / kSegRows + a.nseq * 64;
+// Clears what the pass publishes and plans a packed batch; nothing to do for
+// a dense batch of one tile.
+hipError_t run_plan(GatedArgs& a, const GatedLayout& lay, char* ws, const float* in, float* out, GatedPass* ps,
+                    hipStream_t stream) {
+    const bool many = lay.ntiles > 1;
+    *ps = GatedPass{lay.ntiles, (int32_t)blocks_of(a.C, kTileCh), nullptr, nullptr, nullptr};
+    GatedPlan pl{nullptr, 0, nullptr, 0, nullptr, in, nullptr};
+    if (many) {
+        pl.words = ps->maps = (uint64_t*)(ws + lay.maps);
+        ps->entry = ps->maps + lay.ntiles * a.C;
+        pl.nwords = (lay.ntiles + lay.ngroups) * a.C;
+        pl.counters = ps->counters = (uint32_t*)(ws + lay.counters);
+        pl.ncounters = (int64_t)ps->nblocks * kGatedCounterStride;
+    }
+    if (a.cu && a.T > 0) a.bits = pl.bits = (uint32_t*)(ws + lay.bits);
+    if (a.cu || a.T == 0) pl.out = out;
+    const int64_t items = std::max((a.cu ? (a.T + kBitRows - 1) / kBitRows : 0) + (pl.out ? a.nseq * 64 : 0), pl.nwords / 4);
+    if (!many && !pl.bits && !pl.out) return hipSuccess;
     const unsigned grid = (unsigned)std::min<int64_t>(std::max<int64_t>((items + 255) / 256, 1), 2048);
-    hipLaunchKernelGGL(gated_plan_kernel, dim3(grid), dim3(256), 0, stream, a, bits, in, out);
+    hipLaunchKernelGGL(gated_plan_kernel, dim3(grid), dim3(256), 0, stream, a, pl);
     return hipGetLastError();
 }
 
 template <typename T, typename Y>
 hipError_t run_forward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream_t stream) {
-    uint32_t* bits = a.cu && a.T > 0 ? (uint32_t*)(ws + lay.bits) : nullptr;
-    a.bits = bits;
-    hipError_t e = run_plan(a, bits, a.init, a.final_state, stream);
+    GatedPass ps;
+    const hipError_t e = run_plan(a, lay, ws, a.init, a.final_state, &ps, stream);
     if (e != hipSuccess || a.T == 0) return e;
-    float* states = a.states_out ? a.states_out : (float*)(ws + lay.carry);
-    f32x2* agg = (f32x2*)(ws + lay.agg);
-    const dim3 grid((unsigned)lay.ntiles, blocks_of(a.C, kTileCh));
-    hipLaunchKernelGGL((gated_forward_kernel<T, Y, true>), grid, dim3(kThreads), 0, stream, a, agg, (const float*)nullptr);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((gated_carry_kernel<false>), dim3(blocks_of(a.C, 64)), dim3(64), 0, stream, lay.ntiles, a.C,
-                       (const f32x2*)agg, states);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((gated_forward_kernel<T, Y, false>), grid, dim3(kThreads), 0, stream, a, agg, (const float*)states);
+    hipLaunchKernelGGL((gated_forward_kernel<T, Y>), dim3((unsigned)(lay.ntiles * ps.nblocks)),
+                       dim3(kTileRows / kFwdRows * kSegLanes), 0, stream, a, ps);
     return hipGetLastError();
 }
 
 template <typename T, typename Y>
 hipError_t run_backward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream_t stream) {
-    uint32_t* bits = a.cu && a.T > 0 ? (uint32_t*)(ws + lay.bits) : nullptr;
-    a.bits = bits;
-    hipError_t e = run_plan(a, bits, a.dfinal, a.dinit, stream);
+    GatedPass ps;
+    hipError_t e = run_plan(a, lay, ws, a.dfinal, a.dinit, &ps, stream);
     if (e != hipSuccess) return e;
-    f32x2* agg = (f32x2*)(ws + lay.agg);
-    float* adj = (float*)(ws + lay.carry);
     float* part = (float*)(ws + lay.dlam);
     if (a.T > 0) {
-        const dim3 grid((unsigned)lay.ntiles, blocks_of(a.C, kTileCh));
-        hipLaunchKernelGGL((gated_backward_kernel<T, Y, true>), grid, dim3(kThreads), 0, stream, a, agg,
-                           (const float*)nullptr, (float*)nullptr);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL((gated_carry_kernel<true>), dim3(blocks_of(a.C, 64)), dim3(64), 0, stream, lay.ntiles, a.C,
-                           (const f32x2*)agg, adj);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL((gated_backward_kernel<T, Y, false>), grid, dim3(kThreads), 0, stream, a, agg,
-                           (const float*)adj, part);
+        hipLaunchKernelGGL((gated_backward_kernel<T, Y>), dim3((unsigned)(lay.ntiles * ps.nblocks)),
+                           dim3(kTileRows / kBwdRows * kSegLanes), 0, stream, a, ps, part);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     hipLaunchKernelGGL(gated_dlam_kernel, dim3(blocks_of(a.C, 64)), dim3(1024), 0, stream, a, lay.ntiles,
@@ -485,20 +571,23 @@ hipError_t run_gated_step(const GatedArgs& a, const float* state, float* state_o
 
 }  // namespace
 
-GatedLayout gated_layout(int64_t T, int32_t C, bool packed, bool backward, bool keep_states) {
+GatedLayout gated_layout(int64_t T, int32_t C, bool packed, bool backward) {
     GatedLayout l;
     l.ntiles = (T + kTileRows - 1) / kTileRows;
+    l.ngroups = (l.ntiles + kGroup - 1) / kGroup;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t p = at;
         at += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    l.bits = take(packed ? (size_t)((T + kSegRows - 1) / kSegRows) * 4 : 0);
-    l.agg = take((size_t)l.ntiles * C * 8);
-    l.carry = take(backward || !keep_states ? (size_t)l.ntiles * C * 4 : 0);
+    const bool many = l.ntiles > 1;
+    l.bits = take(packed ? (size_t)((T + kBitRows - 1) / kBitRows) * 4 : 0);
+    l.maps = take(many ? (size_t)(l.ntiles + l.ngroups) * C * 8 : 0);
+    l.counters = take(many ? (size_t)((C + kTileCh - 1) / kTileCh) * kGatedCounterStride * 4 : 0);
     l.dlam = take(backward ? (size_t)l.ntiles * C * 4 : 0);
     l.total = at;
+    l.blocks = l.ntiles * ((C + kTileCh - 1) / kTileCh);
     return l;
 }
 

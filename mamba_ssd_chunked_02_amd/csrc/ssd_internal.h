@@ -216,15 +216,39 @@ struct GatedArgs {
 
 // Byte offsets of the workspace regions (256-byte aligned).
 struct GatedLayout {
-    int64_t ntiles;
-    size_t bits;   // u32 per run of rows (packed)
-    size_t agg;    // f32 x2 [ntiles][C]: every tile's map of the state
-    size_t carry;  // f32 [ntiles][C]: the state (backward: adjoint) entering every tile
-    size_t dlam;   // f32 [ntiles][C]: the tiles' sums of dlam
+    int64_t ntiles, ngroups;
+    int64_t blocks;   // workgroups of the pass
+    size_t bits;      // u32 per 8 rows (packed): sequence boundaries
+    size_t maps;      // u64 [ntiles][C]: every tile's map of the state, then [ngroups][C]: the state entering every group
+    size_t counters;  // u32 per channel block, kGatedCounterStride apart: tiles handed out
+    size_t dlam;      // f32 [ntiles][C]: the tiles' sums of dlam (backward)
     size_t total;
 };
 
-GatedLayout gated_layout(int64_t T, int32_t C, bool packed, bool backward, bool keep_states);
+// Words between the counters of two channel blocks (a cache line).
+constexpr int kGatedCounterStride = 32;
+
+// What a pass over the tiles shares between its workgroups.
+struct GatedPass {
+    int64_t ntiles;
+    int32_t nblocks;     // channel blocks
+    uint64_t* maps;
+    uint64_t* entry;
+    uint32_t* counters;  // NULL: one tile, nothing to share
+};
+
+// What the plan kernel writes.
+struct GatedPlan {
+    uint64_t* words;
+    int64_t nwords;
+    uint32_t* counters;
+    int64_t ncounters;
+    uint32_t* bits;
+    const float* in;
+    float* out;
+};
+
+GatedLayout gated_layout(int64_t T, int32_t C, bool packed, bool backward);
 hipError_t launch_gated_scan(const GatedArgs& a, const GatedLayout& lay, void* ws, hipStream_t stream);
 hipError_t launch_gated_backward(const GatedArgs& a, const GatedLayout& lay, void* ws, hipStream_t stream);
 hipError_t launch_gated_step(const GatedArgs& a, const float* state, float* state_out, hipStream_t stream);
