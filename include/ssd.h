@@ -423,7 +423,7 @@ ssd_status ssd_causal_conv1d_backward(const ssd_conv_outputs* dout, const void* 
  *   ydtype       ssd_dtype of y (and dy)
  *   rate         finite and > 0
  *   x_stride, r_stride, i_stride      elements from one row to the next:
- *                multiples of 8, at least C; 0 means C
+ *                multiples of 8, in [C, 2^22]; 0 means C
  *   dx_stride, dr_stride, di_stride   the same for the gradients (backward only)
  *   reserved     must be 0
  * A packed batch may hold rows behind its last sequence (cu_seqlens[batch] <

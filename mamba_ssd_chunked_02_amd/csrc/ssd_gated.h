@@ -32,7 +32,7 @@ __device__ inline RowRange live_rows(const int32_t* cu, int64_t nseq, int64_t T)
 
 // The sequence holding a live row: the last one that starts at or before it.
 __device__ inline int64_t seq_of(const int32_t* cu, int64_t nseq, int64_t L, int64_t row) {
-    if (!cu) return row / L;
+    if (!cu) return (uint32_t)row / (uint32_t)L;  // rows < 2^31
     int64_t lo = 0, hi = nseq - 1;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) >> 1;
@@ -41,6 +41,31 @@ __device__ inline int64_t seq_of(const int32_t* cu, int64_t nseq, int64_t L, int
     }
     return lo;
 }
+
+// ---------------------------------------------------------------- four channels as loaded
+// bf16 channels stay in the two words they were loaded as (a vector of 16-bit
+// elements that meets a branch takes a register for every element).
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    typedef f32x4 type;
+    __device__ static inline f32x4 widen(f32x4 v) { return v; }
+    __device__ static inline f32x4 all(float v) { return f32x4{v, v, v, v}; }
+};
+template <>
+struct Raw<bf16_t> {
+    typedef uint32_t type __attribute__((ext_vector_type(2)));
+    __device__ static inline f32x4 widen(type v) {
+        return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xffff0000u),
+                     __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xffff0000u)};
+    }
+    // v exact in bf16
+    __device__ static inline type all(float v) {
+        const uint32_t h = __builtin_bit_cast(uint32_t, v), w = h | h >> 16;
+        return type{w, w};
+    }
+};
 
 // ---------------------------------------------------------------- gates
 // sigmoid with the hardware exponential and reciprocal (1 ulp each).
@@ -71,26 +96,62 @@ __device__ inline float expm1_slow(float v) {
     return p * v;
 }
 
-// a = exp(v) and m = 1 - a^2 of one element, from the held decay w: a - 1 (<= 0)
-// where v >= -0.35, elsewhere a itself (> 0), so that neither a nor a - 1 loses
-// digits.  m = -e (1 + a) with e = a - 1 has no cancellation however near a is
-// to 1.  SLOW: every channel of the wave decays by no more than 0.35 a token, so
-// that no element takes the exponential.
-template <bool SLOW>
-__device__ inline float held_decay(float v) {
-    if constexpr (SLOW) return expm1_slow(v);
-    // the floor keeps w > 0 where a underflows
-    const float q = fmaxf(__builtin_amdgcn_exp2f(v * 1.44269504088896341f), 1e-37f);
-    return v < kSlowDecay ? q : expm1_slow(v);
-}
-template <bool SLOW>
-__device__ inline float decay_of(float w) {
-    return !SLOW && w > 0.f ? w : 1.f + w;
-}
-template <bool SLOW>
-__device__ inline float one_minus_a2(float w) {
-    const float e = !SLOW && w > 0.f ? w - 1.f : w;
-    return __builtin_fmaf(-e, decay_of<SLOW>(w), -e);
+// a = exp(v) and m = 1 - a^2 = -e (1 + a), e = a - 1, with no cancellation
+// however near a is to 1, and w, which holds both: e (<= 0) where v >= -0.35,
+// elsewhere a itself (> 0).  slow (the same for a wave): no channel of the wave
+// decays by more than 0.35 a token, so that no element takes the exponential.
+struct Decay {
+    f32x4 a, m, w;
+    __device__ inline void from_log(f32x4 v, bool slow) {
+        if (slow) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[c] = expm1_slow(v[c]);
+                a[c] = 1.f + w[c];
+                m[c] = __builtin_fmaf(-w[c], a[c], -w[c]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // the floor keeps w > 0 where a underflows
+                const float p = expm1_slow(v[c]), q = fmaxf(__builtin_amdgcn_exp2f(v[c] * 1.44269504088896341f), 1e-37f);
+                const bool far = v[c] < kSlowDecay;
+                const float e = far ? q - 1.f : p;
+                a[c] = far ? q : 1.f + p;
+                w[c] = far ? q : p;
+                m[c] = __builtin_fmaf(-e, a[c], -e);
+            }
+        }
+    }
+    __device__ inline void from_held(f32x4 held, bool slow) {
+        if (slow) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                a[c] = 1.f + held[c];
+                m[c] = __builtin_fmaf(-held[c], a[c], -held[c]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float e = held[c] > 0.f ? held[c] - 1.f : held[c];
+                a[c] = held[c] > 0.f ? held[c] : 1.f + held[c];
+                m[c] = __builtin_fmaf(-e, a[c], -e);
+            }
+        }
+    }
+};
+
+// a of a held decay.
+__device__ inline f32x4 decay_of(f32x4 held, bool slow) {
+    f32x4 a;
+    if (slow) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = 1.f + held[c];
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = held[c] > 0.f ? held[c] : 1.f + held[c];
+    }
+    return a;
 }
 
 }  // namespace ssd

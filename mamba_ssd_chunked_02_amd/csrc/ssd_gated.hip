@@ -43,7 +43,7 @@ constexpr int kTileCh = kLaneCh * kSegLanes;    // channels per workgroup
 constexpr int kTileRows = kGatedTileRows;
 constexpr int kGroup = 16;                      // tiles per group of the carry
 constexpr int kBitRows = 8;                     // rows per word of boundary bits
-constexpr int kFwdRows = 8, kBwdRows = 4;       // rows per run (per lane)
+constexpr int kFwdRows = 8, kBwdRows = 8;       // rows per run (per lane)
 constexpr uint64_t kNotYet = ~(uint64_t)0;      // a published word that is not there yet
 
 __device__ inline bool is_reset(float P) { return __builtin_bit_cast(int, P) < 0; }
@@ -126,13 +126,17 @@ __global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, GatedPlan 
 }
 
 // What a lane has of its run of rows: the place, the boundary bits and the
-// live rows (bit j).
+// live rows (bit j).  plain: no run of the wave has a boundary or a row that is
+// not live, and so none of the tests per row is needed.
 template <int ROWS>
 struct Run {
-    int64_t t0;
+    int64_t tile0;   // the tile's first row
+    int row;         // the run's first row in the tile
     int c0;          // first channel (clamped into the row)
     bool on;         // the lane's channels exist
+    int plain;       // (a scalar)
     uint32_t bits, live;
+    __device__ int64_t t(int j) const { return tile0 + row + j; }
     __device__ bool start(int j) const { return bits >> j & 1; }
     __device__ bool end(int j) const { return bits >> (16 + j) & 1; }
     __device__ bool has(int j) const { return live >> j & 1; }
@@ -140,47 +144,130 @@ struct Run {
     __device__ bool any_end() const { return bits >> 16 & live; }
 
     __device__ Run(const GatedArgs& a, int64_t tile, int cb) {
-        t0 = tile * kTileRows + (threadIdx.x / kSegLanes) * ROWS;
+        tile0 = tile * kTileRows;
+        row = (int)(threadIdx.x / kSegLanes) * ROWS;
         const int c = cb * kTileCh + (threadIdx.x % kSegLanes) * kLaneCh;
         on = c < a.C;
         c0 = on ? c : a.C - kLaneCh;
-        bits = t0 < a.T ? boundary_bits<ROWS>(a, t0) : 0;
+        if (!a.cu) {
+            // rows < 2^31; the whole tile between two boundaries, or not
+            const uint32_t p = (uint32_t)tile0 % (uint32_t)a.L;
+            if (p && a.L - p > kTileRows) {
+                bits = 0;
+                live = (1u << ROWS) - 1;
+                plain = 1;
+                return;
+            }
+        }
+        bits = t(0) < a.T ? boundary_bits<ROWS>(a, t(0)) : 0;
         const RowRange r = live_rows(a.cu, a.nseq, a.T);
-        const int lo = (int)min(max(r.lo - t0, (int64_t)0), (int64_t)ROWS);
-        const int hi = (int)min(max(r.hi - t0, (int64_t)lo), (int64_t)ROWS);
+        const int lo = (int)min(max(r.lo - t(0), (int64_t)0), (int64_t)ROWS);
+        const int hi = (int)min(max(r.hi - t(0), (int64_t)lo), (int64_t)ROWS);
         live = ((1u << hi) - 1) & ~((1u << lo) - 1);
+        plain = __builtin_amdgcn_readfirstlane(__all(bits == 0 && live == (1u << ROWS) - 1));
     }
 };
 
+// Row j of the run in a [rows, stride] tensor: a base that is the same for the
+// whole workgroup plus a 32-bit offset of the lane that is the same for every
+// j (strides are at most 2^22 elements).
+template <typename T>
+__device__ inline T* at_row(T* p, int64_t row0, int64_t stride, uint32_t bytes) {
+    return (T*)((char*)(p + row0 * stride) + bytes);
+}
+
+// The data is read once and written once: streaming loads and stores.  A tile
+// that reaches past the last row reads that row instead.
 template <typename T, int ROWS>
 __device__ inline void load_rows(const GatedArgs& a, const Run<ROWS>& u, const void* p, int64_t stride,
-                                 typename Tr<T>::v4 (&v)[ROWS]) {
+                                 typename Raw<T>::type (&v)[ROWS]) {
+    typedef typename Raw<T>::type raw;
+    T* const q = (T*)const_cast<void*>(p);
+    if (u.tile0 + kTileRows <= a.T) {
+        const uint32_t bytes = ((uint32_t)u.row * (uint32_t)stride + (uint32_t)u.c0) * sizeof(T);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) v[j] = __builtin_nontemporal_load((const raw*)at_row(q, u.tile0 + j, stride, bytes));
+    } else {
+        const int last = (int)(a.T - 1 - u.tile0);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+            v[j] = *(const raw*)at_row(
+                q, u.tile0, stride, ((uint32_t)min(u.row + j, last) * (uint32_t)stride + (uint32_t)u.c0) * sizeof(T));
+    }
+}
+
+template <typename T, int ROWS>
+__device__ inline void store_row(const Run<ROWS>& u, void* p, int64_t stride, int j, f32x4 v) {
+    const uint32_t bytes = ((uint32_t)u.row * (uint32_t)stride + (uint32_t)u.c0) * sizeof(T);
+    __builtin_nontemporal_store(Tr<T>::narrow4(v), (typename Tr<T>::v4*)at_row((T*)p, u.tile0 + j, stride, bytes));
+}
+
+__device__ inline int64_t state_at(const GatedArgs& a, int64_t row, int c0) {
+    return seq_of(a.cu, a.nseq, a.L, row) * a.C + c0;
+}
+
+// Rows that are not live become steps that change nothing: log a = 0, x = 0.
+template <typename T, int ROWS>
+__device__ inline void idle_rows(const Run<ROWS>& u, typename Raw<T>::type (&xv)[ROWS], typename Raw<T>::type (&rv)[ROWS],
+                                 typename Raw<T>::type (&iv)[ROWS]) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j)
-        v[j] = Tr<T>::ld4raw((const T*)p + min(u.t0 + j, a.T - 1) * stride + u.c0);
+        if (!u.has(j)) {
+            xv[j] = iv[j] = Raw<T>::all(0.f);
+            rv[j] = Raw<T>::all(-__builtin_inff());
+        }
 }
 
-__device__ inline f32x4 seq_state(const float* st, const GatedArgs& a, int64_t row, int c0) {
-    return st ? *(const f32x4*)(st + seq_of(a.cu, a.nseq, a.L, row) * a.C + c0) : f32x4{};
+__device__ inline f32x4 seq_state(const GatedArgs& a, const float* st, int64_t row, int c0) {
+    return st ? *(const f32x4*)(st + state_at(a, row, c0)) : f32x4{};
 }
 
-// log a, the held decay and b of one row's four channels.
-template <typename T, bool SLOW>
+// The value is computed here and kept, and what it was computed from is
+// forgotten: without this the compiler keeps every row's intermediate values
+// alive for a later use of the same expression, 40 to 90 registers more.
+__device__ inline void pin(f32x4& v) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float t = v[c];
+        asm volatile("" : "+v"(t));
+        v[c] = t;
+    }
+}
+
+// One row: the gates, the held decay, a and b of four channels.
+template <typename T>
 struct Step {
-    f32x4 loga, w, b;
-    __device__ Step(f32x4 k, typename Tr<T>::v4 xv, typename Tr<T>::v4 rv, typename Tr<T>::v4 iv) {
-        const f32x4 x = Tr<T>::widen4(xv), r = Tr<T>::widen4(rv), i = Tr<T>::widen4(iv);
+    f32x4 sr, si, w, a, b;
+    __device__ Step(f32x4 k, bool slow, typename Raw<T>::type xv, typename Raw<T>::type rv, typename Raw<T>::type iv) {
+        const f32x4 x = Raw<T>::widen(xv), r = Raw<T>::widen(rv), i = Raw<T>::widen(iv);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            loga[c] = k[c] * sigmoid_f(r[c]);
-            w[c] = held_decay<SLOW>(loga[c]);
-            b[c] = __builtin_amdgcn_sqrtf(one_minus_a2<SLOW>(w[c])) * sigmoid_f(i[c]) * x[c];
+            sr[c] = sigmoid_f(r[c]);
+            si[c] = sigmoid_f(i[c]);
         }
+        Decay d;
+        d.from_log(k * sr, slow);
+        w = d.w;
+        a = d.a;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = __builtin_amdgcn_sqrtf(d.m[c]) * si[c] * x[c];
     }
 };
-template <bool SLOW>
-__device__ inline f32x4 decay4(f32x4 w) {
-    return f32x4{decay_of<SLOW>(w[0]), decay_of<SLOW>(w[1]), decay_of<SLOW>(w[2]), decay_of<SLOW>(w[3])};
+
+// At a sequence's first row the initial state goes into b and the state before
+// it counts as 0: H goes on from (a, b) of row j.
+template <int ROWS>
+__device__ inline void take_row(const GatedArgs& a, const Run<ROWS>& u, int j, f32x4 av, f32x4& b, f32x4& H) {
+    if (!u.plain)
+        if (u.start(j)) {
+            b += av * seq_state(a, a.init, u.t(j), u.c0);
+            H = f32x4{};
+        }
+    H = av * H + b;
+}
+
+__device__ inline int slow_wave(f32x4 k) {
+    return __builtin_amdgcn_readfirstlane(!__any(fminf(fminf(k[0], k[1]), fminf(k[2], k[3])) < kSlowDecay));
 }
 
 // A run's factor from its sum of log a.
@@ -294,30 +381,28 @@ __global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forwar
         k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
     const int64_t tile = next_tile(ps, cb, &slot);
     const Run<R> u(a, tile, cb);
-    typename Tr<T>::v4 xv[R], rv[R], iv[R];
+    typename Raw<T>::type xv[R], rv[R], iv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
     load_rows<T>(a, u, a.i, a.i_stride, iv);
     load_rows<T>(a, u, a.x, a.x_stride, xv);
     __syncthreads();
     const f32x4 k = *(const f32x4*)(k_s + ln * kLaneCh);
 
+    if (!u.plain) idle_rows<T>(u, xv, rv, iv);
+    const int slow = slow_wave(k);
     f32x4 av[R], b[R], S = {}, H = {};
-    auto local = [&](auto slow) {
-        constexpr bool SLOW = decltype(slow)::value;
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const Step<T, SLOW> st(k, xv[j], rv[j], iv[j]);
-            av[j] = decay4<SLOW>(st.w);
-            b[j] = st.b;
-            if (u.has(j)) {
-                if (u.start(j)) H = seq_state(a.init, a, u.t0 + j, u.c0);
-                S += st.loga;
-                H = av[j] * H + b[j];
-            }
-        }
-    };
-    if (__any(fminf(fminf(k[0], k[1]), fminf(k[2], k[3])) < kSlowDecay)) local(std::false_type{});
-    else local(std::true_type{});
+    for (int j = 0; j < R; ++j) {
+        const Step<T> st(k, slow, xv[j], rv[j], iv[j]);
+        S += st.sr;
+        av[j] = st.a;
+        b[j] = st.b;
+        take_row(a, u, j, av[j], b[j], H);
+        pin(av[j]);
+        pin(b[j]);
+        pin(S);
+    }
+    S *= k;
     P_s[seg][ln] = run_factor(S, u.any_start());
     H_s[seg][ln] = H;
     __syncthreads();
@@ -337,12 +422,14 @@ __global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forwar
     f32x4 h = H_s[seg][ln];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        if (!u.has(j)) continue;
-        if (u.start(j)) h = seq_state(a.init, a, u.t0 + j, u.c0);
-        h = av[j] * h + b[j];
-        Tr<Y>::st4((Y*)a.y + (u.t0 + j) * a.C + u.c0, h);
-        if (a.final_state && u.end(j))
-            *(f32x4*)(a.final_state + seq_of(a.cu, a.nseq, a.L, u.t0 + j) * a.C + u.c0) = h;
+        if (u.plain) {
+            h = av[j] * h + b[j];
+            store_row<Y>(u, a.y, a.C, j, h);
+        } else if (u.has(j)) {
+            h = av[j] * (u.start(j) ? f32x4{} : h) + b[j];
+            store_row<Y>(u, a.y, a.C, j, h);
+            if (a.final_state && u.end(j)) *(f32x4*)(a.final_state + state_at(a, u.t(j), u.c0)) = h;
+        }
     }
 }
 
@@ -369,8 +456,8 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
         k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
     const int64_t ord = next_tile(ps, cb, &slot), tile = ps.ntiles - 1 - ord;
     const Run<R> u(a, tile, cb);
-    typename Tr<T>::v4 xv[R], rv[R], iv[R];
-    typename Tr<Y>::v4 dv[R];
+    typename Raw<T>::type xv[R], rv[R], iv[R];
+    typename Raw<Y>::type dv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
     load_rows<Y>(a, u, a.dy, a.C, dv);
     load_rows<T>(a, u, a.i, a.i_stride, iv);
@@ -380,31 +467,35 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
     const float state0 = threadIdx.x >> 6 == 1 && chan < a.C ? a.states_in[tile * a.C + chan] : 0.f;
     __syncthreads();
     const f32x4 k = *(const f32x4*)(k_s + ln * kLaneCh);
-    const bool slow_wave = !__any(fminf(fminf(k[0], k[1]), fminf(k[2], k[3])) < kSlowDecay);
-
-    f32x4 w[R], b[R], S = {}, H = {}, Q = {};
-    auto local = [&](auto slow) {
-        constexpr bool SLOW = decltype(slow)::value;
+    const int slow = slow_wave(k);
+    if (!u.plain) idle_rows<T>(u, xv, rv, iv);
+    f32x4 w[R], b[R], sr[R], si[R], S = {}, H = {}, Q = {};
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const Step<T, SLOW> st(k, xv[j], rv[j], iv[j]);
-            w[j] = st.w;
-            b[j] = st.b;
-            if (u.has(j)) {
-                if (u.start(j)) H = seq_state(a.init, a, u.t0 + j, u.c0);
-                S += st.loga;
-                H = decay4<SLOW>(st.w) * H + b[j];
-            }
+    for (int j = 0; j < R; ++j) {
+        const Step<T> st(k, slow, xv[j], rv[j], iv[j]);
+        S += st.sr;
+        sr[j] = st.sr;
+        si[j] = st.si;
+        w[j] = st.w;
+        b[j] = st.b;
+        take_row(a, u, j, st.a, b[j], H);
+        pin(sr[j]);
+        pin(si[j]);
+        pin(w[j]);
+        pin(b[j]);
+        pin(S);
+    }
+    S *= k;
+#pragma unroll
+    for (int j = R - 1; j >= 0; --j) {
+        f32x4 g = Raw<Y>::widen(dv[j]);
+        if (!u.plain) {
+            if (!u.has(j)) continue;
+            if (u.end(j)) Q = seq_state(a, a.dfinal, u.t(j), u.c0);
         }
-#pragma unroll
-        for (int j = R - 1; j >= 0; --j)
-            if (u.has(j)) {
-                if (u.end(j)) Q = seq_state(a.dfinal, a, u.t0 + j, u.c0);
-                Q = decay4<SLOW>(w[j]) * (Q + Tr<Y>::widen4(dv[j]));
-            }
-    };
-    if (slow_wave) local(std::true_type{});
-    else local(std::false_type{});
+        Q = decay_of(w[j], slow) * (Q + g);
+        pin(w[j]);
+    }
     P_s[seg][ln] = run_factor(S, u.any_start());
     H_s[seg][ln] = H;
     R_s[seg][ln] = run_factor(S, u.any_end());
@@ -422,47 +513,49 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
     __syncthreads();
 
     f32x4 h = H_s[seg][ln], q = Q_s[seg][ln], dl = {};
-    auto finish = [&](auto slow) {
-        constexpr bool SLOW = decltype(slow)::value;
+    // b: the state before each row from here on
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (u.has(j)) {
-                if (u.start(j)) h = seq_state(a.init, a, u.t0 + j, u.c0);
-                const f32x4 n = decay4<SLOW>(w[j]) * h + b[j];
-                b[j] = h;  // from here on the state before the row
-                h = n;
-            }
+    for (int j = 0; j < R; ++j) {
+        if (!u.plain && u.start(j)) h = f32x4{};
+        const f32x4 n = decay_of(w[j], slow) * h + b[j];
+        b[j] = h;
+        if (!u.plain && u.start(j)) b[j] = seq_state(a, a.init, u.t(j), u.c0);
+        h = n;
+        pin(w[j]);
+    }
 #pragma unroll
-        for (int j = R - 1; j >= 0; --j) {
+    for (int j = R - 1; j >= 0; --j) {
+        if (!u.plain) {
             if (!u.has(j)) continue;
-            if (u.end(j)) q = seq_state(a.dfinal, a, u.t0 + j, u.c0);
-            const f32x4 g = q + Tr<Y>::widen4(dv[j]);
-            q = decay4<SLOW>(w[j]) * g;
-            const f32x4 x = Tr<T>::widen4(xv[j]), r = Tr<T>::widen4(rv[j]), i = Tr<T>::widen4(iv[j]);
-            f32x4 dx, di, dr;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float sr = sigmoid_f(r[c]), si = sigmoid_f(i[c]), av = decay_of<SLOW>(w[j][c]);
-                // 1 - a^2 = 0 only where log a is 0, and its square root's reciprocal meets that factor below;
-                // a floor (the least normal number) keeps their product 0 (a NaN passes)
-                const float m0 = one_minus_a2<SLOW>(w[j][c]), m = m0 < 0x1p-126f ? 0x1p-126f : m0;
-                const float rb = __builtin_amdgcn_rsqf(m), beta = m0 * rb;
-                const float dl0 = g[c] * av * (b[j][c] - av * rb * si * x[c]) * (k[c] * sr);
-                dx[c] = g[c] * beta * si;
-                di[c] = dx[c] * x[c] * (1.f - si);
-                dr[c] = dl0 * (1.f - sr);
-                dl[c] += dl0;
-            }
-            if (!u.on) continue;
-            Tr<T>::st4((T*)a.dx + (u.t0 + j) * a.dx_stride + u.c0, dx);
-            Tr<T>::st4((T*)a.dr + (u.t0 + j) * a.dr_stride + u.c0, dr);
-            Tr<T>::st4((T*)a.di + (u.t0 + j) * a.di_stride + u.c0, di);
-            if (a.dinit && u.start(j))
-                *(f32x4*)(a.dinit + seq_of(a.cu, a.nseq, a.L, u.t0 + j) * a.C + u.c0) = q;
+            if (u.end(j)) q = seq_state(a, a.dfinal, u.t(j), u.c0);
         }
-    };
-    if (slow_wave) finish(std::true_type{});
-    else finish(std::false_type{});
+        const f32x4 x = Raw<T>::widen(xv[j]);
+        const f32x4 g = q + Raw<Y>::widen(dv[j]);
+        Decay d;
+        d.from_held(w[j], slow);
+        q = d.a * g;
+        f32x4 dx, di, dr;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            // 1 - a^2 = 0 only where log a is 0, and its square root's reciprocal meets that factor below;
+            // a floor (the least normal number) keeps their product 0 (a NaN passes)
+            const float m = d.m[c] < 0x1p-126f ? 0x1p-126f : d.m[c];
+            const float rb = __builtin_amdgcn_rsqf(m), beta = d.m[c] * rb;
+            const float dl0 = q[c] * (b[j][c] - d.a[c] * rb * si[j][c] * x[c]) * (k[c] * sr[j][c]);
+            dx[c] = g[c] * beta * si[j][c];
+            di[c] = dx[c] * x[c] * (1.f - si[j][c]);
+            dr[c] = dl0 * (1.f - sr[j][c]);
+            dl[c] += dl0;
+        }
+        pin(q);
+        pin(dl);
+        if (u.on) {
+            store_row<T>(u, a.dx, a.dx_stride, j, dx);
+            store_row<T>(u, a.dr, a.dr_stride, j, dr);
+            store_row<T>(u, a.di, a.di_stride, j, di);
+            if (!u.plain && a.dinit && u.start(j)) *(f32x4*)(a.dinit + state_at(a, u.t(j), u.c0)) = q;
+        }
+    }
     __syncthreads();
     P_s[seg][ln] = dl;
     __syncthreads();
@@ -500,12 +593,12 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a, const floa
     const int64_t n = id / quads;
     const int c0 = (int)(id - n * quads) * kLaneCh;
     f32x4 h = *(const f32x4*)(state + n * a.C + c0), k = *(const f32x4*)(a.lam + c0);
-    const Step<T, false> st((f32x4){decay_factor(k[0], a.rate), decay_factor(k[1], a.rate), decay_factor(k[2], a.rate),
-                             decay_factor(k[3], a.rate)},
-                     Tr<T>::ld4raw((const T*)a.x + n * a.x_stride + c0),
-                     Tr<T>::ld4raw((const T*)a.r + n * a.r_stride + c0),
-                     Tr<T>::ld4raw((const T*)a.i + n * a.i_stride + c0));
-    h = decay4<false>(st.w) * h + st.b;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) k[c] = decay_factor(k[c], a.rate);
+    typedef typename Raw<T>::type raw;
+    const Step<T> st(k, false, *(const raw*)((const T*)a.x + n * a.x_stride + c0),
+                     *(const raw*)((const T*)a.r + n * a.r_stride + c0), *(const raw*)((const T*)a.i + n * a.i_stride + c0));
+    h = st.a * h + st.b;
     *(f32x4*)(state_out + n * a.C + c0) = h;
     Tr<Y>::st4((Y*)a.y + n * a.C + c0, h);
 }
