@@ -18,8 +18,7 @@ import ctypes
 import math
 from typing import Optional, Sequence
 
-from . import (_check, _conv_outputs, _ConvShape, _dtype_code, _dtype_code_of, _expect, _ptr, _stream_handle, _torch,
-               load)
+from . import (SSD_BF16, SSD_F32, SsdError, _conv_outputs, _ConvShape, _dtype_code_of, _expect, _torch, load)
 
 __all__ = ["gated_scan", "gated_scan_step", "gated_scan_backward", "add_rms_norm", "add_rms_norm_backward",
            "gated_rms_norm", "gated_rms_norm_backward", "causal_conv1d_backward", "GATED_TILE_ROWS"]
@@ -42,13 +41,14 @@ class _NormShape(ctypes.Structure):
                 ("dx_stride", ctypes.c_int64), ("dz_stride", ctypes.c_int64), ("reserved", ctypes.c_int64)]
 
 
-_declared = False
+_functions = {}
+_codes = {}  # torch dtype -> ssd_dtype
 
 
 def _lib():
-    global _declared
+    """The library, with the entry points below declared."""
     lib = load()
-    if not _declared:
+    if not _functions:
         vp, sz = ctypes.c_void_p, ctypes.c_size_t
         szp = ctypes.POINTER(sz)
         gsp, nsp, csp = (ctypes.POINTER(t) for t in (_GatedShape, _NormShape, _ConvShape))
@@ -67,26 +67,62 @@ def _lib():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_int32
-        _declared = True
+            _functions[name] = f
+        torch = _torch()
+        _codes.update({torch.float32: SSD_F32, torch.bfloat16: SSD_BF16})
     return lib
 
 
-def _same_device(first, *others):
-    """All tensors on one GPU; returns that device."""
-    for t in (first,) + others:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU")
-        if t.device != first.device:
+def _fail(status, name):
+    raise SsdError(status, name, load().ssd_last_error_detail().decode())
+
+
+def _launch(index, name, *args):
+    """Calls an entry point on the device's current stream, with the device current."""
+    torch = _torch()
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        st = _functions[name](*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = _functions[name](*args, stream)
+    if st:
+        _fail(st, name)
+
+
+def _query(name, *args) -> int:
+    need = ctypes.c_size_t(0)
+    st = _functions[name](*args, ctypes.byref(need))
+    if st:
+        _fail(st, name)
+    return need.value
+
+
+def _gpu(first, *others) -> int:
+    """All tensors on one GPU; returns its index."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on the GPU")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            if not t.is_cuda:
+                raise ValueError("tensors must live on the GPU")
             raise ValueError("tensors live on %s and %s" % (first.device, t.device))
-    return first.device
+    if not _functions:
+        _lib()
+    return index
+
+
+def _code(dtype) -> int:
+    code = _codes.get(dtype)
+    return _dtype_code_of(dtype) if code is None else code
 
 
 def _row_stride(t, name) -> int:
-    """Elements from one row [C] of t to the next; the rows of all leading
-    dimensions must lie at one distance (a column range of a wider tensor does)."""
-    if t.numel() == 0:
+    """Elements from one row [C] of t to the next, 0 where the rows are dense; the
+    rows of all leading dimensions must lie at one distance (a column range of
+    a wider tensor does)."""
+    if t.is_contiguous():
         return 0
     if t.shape[-1] != 1 and t.stride(-1) != 1:
         raise ValueError("the last dimension of %s must be contiguous" % name)
@@ -106,25 +142,31 @@ def _row_stride(t, name) -> int:
 
 def _shaped(t, shape, dtype, name):
     """Shape and dtype; the strides are free."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
 
 
-def _out(t, shape, dtype, name, device):
-    """A given output, checked, or a new one."""
-    torch = _torch()
-    if t is None:
-        return torch.empty(tuple(shape), dtype=dtype, device=device)
-    _shaped(t, shape, dtype, name)
-    return t
+def _need(t, shape, dtype, name):
+    """Shape, dtype and dense strides of a tensor that may be None."""
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+        _expect(t, shape, dtype, name)
 
 
-def _workspace(given, need, device):
-    torch = _torch()
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _new(like, shape, dtype):
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(given, need, like):
     if given is None or given.numel() * given.element_size() < need:
-        return torch.empty(int(need), dtype=torch.uint8, device=device)
+        return _new(like, (need,), _torch().uint8)
+    if not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return given
 
 
@@ -134,7 +176,6 @@ def _bytes(w) -> int:
 
 def _sequences(sh, x, cu_seqlens, cu_seqlens_host):
     """Fills batch, seqlen and the offsets of a shape from x [b, L, C] or [T, C]; returns what must stay alive."""
-    torch = _torch()
     if cu_seqlens is None:
         if x.dim() != 3:
             raise ValueError("dense tensors must be [b, L, C]")
@@ -146,7 +187,7 @@ def _sequences(sh, x, cu_seqlens, cu_seqlens_host):
         raise ValueError("packed tensors must be [T, C]")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [nseq + 1]")
-    _expect(cu_seqlens, (cu_seqlens.shape[0],), torch.int32, "cu_seqlens")
+    _need(cu_seqlens, cu_seqlens.shape, _torch().int32, "cu_seqlens")
     sh.batch, sh.seqlen = cu_seqlens.shape[0] - 1, x.shape[0]
     sh.cu_seqlens = cu_seqlens.data_ptr()
     if cu_seqlens_host is None:
@@ -161,17 +202,12 @@ def _sequences(sh, x, cu_seqlens, cu_seqlens_host):
 
 # ------------------------------------------------------------------ gated recurrence
 def _gated_shape(x, r, i, lam, rate, y_dtype):
-    torch = _torch()
-    sh = _GatedShape()
-    C = x.shape[-1]
-    sh.channels = C
-    sh.dtype, sh.ydtype = _dtype_code(x), _dtype_code_of(y_dtype)
-    sh.rate = float(rate)
-    for name, t in (("x", x), ("r", r), ("i", i)):
-        _shaped(t, x.shape, x.dtype, name)
-        setattr(sh, name + "_stride", _row_stride(t, name))
-    _expect(lam, (C,), torch.float32, "lam")
-    return sh
+    C, dtype = x.shape[-1], x.dtype
+    _shaped(r, x.shape, dtype, "r")
+    _shaped(i, x.shape, dtype, "i")
+    _need(lam, (C,), _torch().float32, "lam")
+    return _GatedShape(0, 0, C, _code(dtype), _code(y_dtype), rate, _row_stride(x, "x"), _row_stride(r, "r"),
+                       _row_stride(i, "i"))
 
 
 def gated_scan(x, r, i, lam, *, rate: float = 8.0, init_state=None, cu_seqlens=None,
@@ -191,32 +227,31 @@ def gated_scan(x, r, i, lam, *, rate: float = 8.0, init_state=None, cu_seqlens=N
 
     A sequence of no tokens passes its state through.  Rows behind the last
     sequence of a packed batch are left as they were in y."""
-    torch = _torch()
-    dev = _same_device(x, r, i, lam, init_state, cu_seqlens, y, final_state, workspace)
+    index = _gpu(x, r, i, lam, init_state, cu_seqlens, y, final_state, workspace)
+    f32 = _torch().float32
     if y_dtype is None:
         y_dtype = x.dtype if y is None else y.dtype
     sh = _gated_shape(x, r, i, lam, rate, y_dtype)
     keep = _sequences(sh, x, cu_seqlens, cu_seqlens_host)
-    n, C, rows = sh.batch, sh.channels, math.prod(x.shape[:-1])
-    _expect(init_state, (n, C), torch.float32, "init_state")
-    _expect(y, x.shape, y_dtype, "y")
-    _expect(final_state, (n, C), torch.float32, "final_state")
-    lib = _lib()
-    with torch.cuda.device(dev):
-        y = _out(y, x.shape, y_dtype, "y", dev)
-        if final_state is None and want_final:
-            final_state = torch.empty((n, C), dtype=torch.float32, device=dev)
-        states = None
-        if want_states:
-            states = torch.empty((-(-rows // GATED_TILE_ROWS), C), dtype=torch.float32, device=dev)
-        need = ctypes.c_size_t(0)
-        _check(lib.ssd_gated_scan_workspace_size(ctypes.byref(sh), 0, ctypes.byref(need)), "ssd_gated_scan_workspace_size")
-        workspace = _workspace(workspace, need.value, dev)
-        _check(lib.ssd_gated_scan(x.data_ptr(), r.data_ptr(), i.data_ptr(), _ptr(lam), _ptr(init_state), _ptr(y),
-                                  _ptr(final_state), _ptr(states), ctypes.byref(sh), _ptr(workspace),
-                                  _bytes(workspace), _stream_handle(x)), "ssd_gated_scan")
+    state = (sh.batch, sh.channels)
+    _need(init_state, state, f32, "init_state")
+    _need(y, x.shape, y_dtype, "y")
+    _need(final_state, state, f32, "final_state")
+    if y is None:
+        y = _new(x, x.shape, y_dtype)
+    if final_state is None and want_final:
+        final_state = _new(x, state, f32)
+    states = _new(x, _states_shape(x), f32) if want_states else None
+    ref = ctypes.byref(sh)
+    workspace = _workspace(workspace, _query("ssd_gated_scan_workspace_size", ref, 0), x)
+    _launch(index, "ssd_gated_scan", x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _p(init_state),
+            y.data_ptr(), _p(final_state), _p(states), ref, workspace.data_ptr(), _bytes(workspace))
     del keep
     return (y, final_state, states) if want_states else (y, final_state)
+
+
+def _states_shape(x):
+    return -(-math.prod(x.shape[:-1]) // GATED_TILE_ROWS), x.shape[-1]
 
 
 def gated_scan_backward(dy, x, r, i, lam, states, *, rate: float = 8.0, init_state=None, dfinal_state=None,
@@ -228,35 +263,35 @@ def gated_scan_backward(dy, x, r, i, lam, states, *, rate: float = 8.0, init_sta
     returned by it.  Returns (dx, dr, di, dlam, dinit_state); dx, dr and di may
     be given as column ranges of one wider tensor.  Rows behind the last
     sequence of a packed batch are left as they were in dx, dr and di."""
-    torch = _torch()
-    dev = _same_device(x, dy, r, i, lam, states, init_state, dfinal_state, cu_seqlens, dx, dr, di, dlam, dinit_state,
-                       workspace)
+    index = _gpu(x, dy, r, i, lam, states, init_state, dfinal_state, cu_seqlens, dx, dr, di, dlam, dinit_state,
+                 workspace)
+    f32 = _torch().float32
     sh = _gated_shape(x, r, i, lam, rate, dy.dtype)
     keep = _sequences(sh, x, cu_seqlens, cu_seqlens_host)
-    n, C, rows = sh.batch, sh.channels, math.prod(x.shape[:-1])
-    _expect(dy, x.shape, dy.dtype, "dy")
-    _expect(states, (-(-rows // GATED_TILE_ROWS), C), torch.float32, "states")
-    _expect(init_state, (n, C), torch.float32, "init_state")
-    _expect(dfinal_state, (n, C), torch.float32, "dfinal_state")
-    _expect(dlam, (C,), torch.float32, "dlam")
-    _expect(dinit_state, (n, C), torch.float32, "dinit_state")
-    lib = _lib()
-    with torch.cuda.device(dev):
-        grads = []
-        for name, t in (("dx", dx), ("dr", dr), ("di", di)):
-            t = _out(t, x.shape, x.dtype, name, dev)
+    state = (sh.batch, sh.channels)
+    _need(dy, x.shape, dy.dtype, "dy")
+    _need(states, _states_shape(x), f32, "states")
+    _need(init_state, state, f32, "init_state")
+    _need(dfinal_state, state, f32, "dfinal_state")
+    _need(dlam, lam.shape, f32, "dlam")
+    _need(dinit_state, state, f32, "dinit_state")
+    grads = []
+    for name, t in (("dx", dx), ("dr", dr), ("di", di)):
+        if t is None:
+            t = _new(x, x.shape, x.dtype)
+        else:
+            _shaped(t, x.shape, x.dtype, name)
             setattr(sh, name + "_stride", _row_stride(t, name))
-            grads.append(t)
-        dlam = _out(dlam, (C,), torch.float32, "dlam", dev)
-        if dinit_state is None and want_dinit:
-            dinit_state = torch.empty((n, C), dtype=torch.float32, device=dev)
-        need = ctypes.c_size_t(0)
-        _check(lib.ssd_gated_scan_workspace_size(ctypes.byref(sh), 1, ctypes.byref(need)), "ssd_gated_scan_workspace_size")
-        workspace = _workspace(workspace, need.value, dev)
-        _check(lib.ssd_gated_scan_backward(_ptr(dy), _ptr(dfinal_state), x.data_ptr(), r.data_ptr(), i.data_ptr(),
-                                           _ptr(lam), _ptr(init_state), _ptr(states), *[t.data_ptr() for t in grads],
-                                           _ptr(dlam), _ptr(dinit_state), ctypes.byref(sh), _ptr(workspace),
-                                           _bytes(workspace), _stream_handle(x)), "ssd_gated_scan_backward")
+        grads.append(t)
+    if dlam is None:
+        dlam = _new(lam, lam.shape, f32)
+    if dinit_state is None and want_dinit:
+        dinit_state = _new(x, state, f32)
+    ref = ctypes.byref(sh)
+    workspace = _workspace(workspace, _query("ssd_gated_scan_workspace_size", ref, 1), x)
+    _launch(index, "ssd_gated_scan_backward", dy.data_ptr(), _p(dfinal_state), x.data_ptr(), r.data_ptr(),
+            i.data_ptr(), lam.data_ptr(), _p(init_state), states.data_ptr(), *[t.data_ptr() for t in grads],
+            dlam.data_ptr(), _p(dinit_state), ref, workspace.data_ptr(), _bytes(workspace))
     del keep
     return (*grads, dlam, dinit_state)
 
@@ -265,40 +300,29 @@ def gated_scan_step(state, x, r, i, lam, *, rate: float = 8.0, state_out=None, y
     """One token per sequence: x, r, i [b, C]; ``state`` [b, C] fp32 is updated
     in place, or left as it is and the new one written to ``state_out``.
     Returns y [b, C], of x's dtype unless ``y_dtype`` says otherwise."""
-    torch = _torch()
-    dev = _same_device(x, r, i, lam, state, state_out, y)
+    index = _gpu(x, r, i, lam, state, state_out, y)
+    f32 = _torch().float32
     if x.dim() != 2:
         raise ValueError("one token per sequence: x must be [b, C]")
     if y_dtype is None:
         y_dtype = x.dtype if y is None else y.dtype
     sh = _gated_shape(x, r, i, lam, rate, y_dtype)
-    sh.batch, sh.seqlen = x.shape[0], 1
-    _expect(state, x.shape, torch.float32, "state")
-    _expect(state_out, x.shape, torch.float32, "state_out")
-    _expect(y, x.shape, y_dtype, "y")
-    with torch.cuda.device(dev):
-        y = _out(y, x.shape, y_dtype, "y", dev)
-        _check(_lib().ssd_gated_scan_step(_ptr(state), _ptr(state if state_out is None else state_out), x.data_ptr(),
-                                          r.data_ptr(), i.data_ptr(), _ptr(lam), _ptr(y), ctypes.byref(sh),
-                                          _stream_handle(x)), "ssd_gated_scan_step")
+    sh.batch = x.shape[0]
+    _expect(state, x.shape, f32, "state")
+    _need(state_out, x.shape, f32, "state_out")
+    _need(y, x.shape, y_dtype, "y")
+    if y is None:
+        y = _new(x, x.shape, y_dtype)
+    _launch(index, "ssd_gated_scan_step", state.data_ptr(), (state if state_out is None else state_out).data_ptr(),
+            x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), y.data_ptr(), ctypes.byref(sh))
     return y
 
 
 # ------------------------------------------------------------------ norms
-def _norm_shape(rows, D, dtype, dtype2, eps, groups=1, norm_before_gate=False):
-    sh = _NormShape()
-    sh.rows, sh.columns, sh.groups = rows, D, int(groups)
-    sh.dtype, sh.dtype2 = _dtype_code_of(dtype), _dtype_code_of(dtype2)
-    sh.eps = float(eps)
-    sh.norm_before_gate = 1 if norm_before_gate else 0
-    return sh
-
-
-def _norm_workspace(sh, workspace, device):
-    need = ctypes.c_size_t(0)
-    _check(_lib().ssd_norm_backward_workspace_size(ctypes.byref(sh), ctypes.byref(need)),
-           "ssd_norm_backward_workspace_size")
-    return _workspace(workspace, need.value, device)
+def _norm_shape(t, dtype, dtype2, eps, groups=1, norm_before_gate=False, x_stride=0, z_stride=0):
+    D = t.shape[-1]
+    return _NormShape(t.numel() // D if D else 0, D, groups, _code(dtype), _code(dtype2), eps,
+                      1 if norm_before_gate else 0, x_stride, z_stride)
 
 
 def add_rms_norm(x, residual, weight, *, scale=None, eps: float = 1e-5, y=None, residual_out=None,
@@ -312,22 +336,22 @@ def add_rms_norm(x, residual, weight, *, scale=None, eps: float = 1e-5, y=None, 
     residual itself.  The norm is that of the fp32 sum, before residual_out is
     rounded.  Returns (y, residual_out), or (y, residual_out, rstd [...] fp32)
     with ``want_rstd``, which add_rms_norm_backward needs."""
-    torch = _torch()
-    dev = _same_device(x, residual, weight, scale, y, residual_out)
-    D, lead = x.shape[-1], x.shape[:-1]
-    _expect(x, x.shape, x.dtype, "x")
-    _expect(residual, x.shape, residual.dtype, "residual")
-    _expect(weight, (D,), torch.float32, "weight")
-    _expect(scale, (D,), torch.float32, "scale")
-    _expect(y, x.shape, x.dtype, "y")
-    _expect(residual_out, x.shape, residual.dtype, "residual_out")
-    sh = _norm_shape(math.prod(lead), D, x.dtype, residual.dtype, eps)
-    with torch.cuda.device(dev):
-        y = _out(y, x.shape, x.dtype, "y", dev)
-        residual_out = _out(residual_out, x.shape, residual.dtype, "residual_out", dev)
-        rstd = torch.empty(tuple(lead), dtype=torch.float32, device=dev) if want_rstd else None
-        _check(_lib().ssd_add_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(scale), _ptr(y), _ptr(residual_out),
-                                       _ptr(rstd), ctypes.byref(sh), _stream_handle(x)), "ssd_add_rms_norm")
+    index = _gpu(x, residual, weight, scale, y, residual_out)
+    f32, shape, dtype, rdtype = _torch().float32, x.shape, x.dtype, residual.dtype
+    _need(x, shape, dtype, "x")
+    _need(residual, shape, rdtype, "residual")
+    _need(weight, shape[-1:], f32, "weight")
+    _need(scale, shape[-1:], f32, "scale")
+    _need(y, shape, dtype, "y")
+    _need(residual_out, shape, rdtype, "residual_out")
+    sh = _norm_shape(x, dtype, rdtype, eps)
+    if y is None:
+        y = _new(x, shape, dtype)
+    if residual_out is None:
+        residual_out = _new(x, shape, rdtype)
+    rstd = _new(x, shape[:-1], f32) if want_rstd else None
+    _launch(index, "ssd_add_rms_norm", x.data_ptr(), residual.data_ptr(), weight.data_ptr(), _p(scale), y.data_ptr(),
+            residual_out.data_ptr(), _p(rstd), ctypes.byref(sh))
     return (y, residual_out, rstd) if want_rstd else (y, residual_out)
 
 
@@ -338,48 +362,41 @@ def add_rms_norm_backward(dy, residual_out, weight, rstd, *, dresidual_out=None,
     ``scale``, x is needed for its gradient.  Returns (dx, dresidual, dweight,
     dscale or None); without a scale and with one dtype dx and dresidual are
     the same tensor unless both are given."""
-    torch = _torch()
-    dev = _same_device(dy, residual_out, weight, rstd, dresidual_out, x, scale, dx, dresidual, workspace)
-    D = dy.shape[-1]
+    index = _gpu(dy, residual_out, weight, rstd, dresidual_out, x, scale, dx, dresidual, workspace)
+    f32, shape, dtype, rdtype = _torch().float32, dy.shape, dy.dtype, residual_out.dtype
     if scale is not None and x is None:
         raise ValueError("the gradient of scale needs x")
-    rdt = residual_out.dtype
-    _expect(dy, dy.shape, dy.dtype, "dy")
-    _expect(residual_out, dy.shape, rdt, "residual_out")
-    _expect(weight, (D,), torch.float32, "weight")
-    _expect(rstd, dy.shape[:-1], torch.float32, "rstd")
-    _expect(dresidual_out, dy.shape, rdt, "dresidual_out")
-    _expect(x, dy.shape, dy.dtype, "x")
-    _expect(scale, (D,), torch.float32, "scale")
-    _expect(dx, dy.shape, dy.dtype, "dx")
-    _expect(dresidual, dy.shape, rdt, "dresidual")
-    sh = _norm_shape(math.prod(dy.shape[:-1]), D, dy.dtype, rdt, 0.0)
-    with torch.cuda.device(dev):
-        one = scale is None and rdt == dy.dtype and (dx is None or dresidual is None)
-        if one:
-            dx = dresidual = _out(dx if dresidual is None else dresidual, dy.shape, rdt, "dx", dev)
-        else:
-            dx = _out(dx, dy.shape, dy.dtype, "dx", dev)
-            dresidual = _out(dresidual, dy.shape, rdt, "dresidual", dev)
-        dweight = torch.empty(D, dtype=torch.float32, device=dev)
-        dscale = None if scale is None else torch.empty(D, dtype=torch.float32, device=dev)
-        workspace = _norm_workspace(sh, workspace, dev)
-        _check(_lib().ssd_add_rms_norm_backward(
-            _ptr(dy), _ptr(dresidual_out), _ptr(residual_out), _ptr(weight), _ptr(rstd),
-            None if scale is None else _ptr(x), _ptr(scale), _ptr(dx), None if one else _ptr(dresidual), _ptr(dweight),
-            _ptr(dscale), ctypes.byref(sh), _ptr(workspace), _bytes(workspace), _stream_handle(dy)),
-            "ssd_add_rms_norm_backward")
+    _need(dy, shape, dtype, "dy")
+    _need(residual_out, shape, rdtype, "residual_out")
+    _need(weight, shape[-1:], f32, "weight")
+    _need(rstd, shape[:-1], f32, "rstd")
+    _need(dresidual_out, shape, rdtype, "dresidual_out")
+    _need(x, shape, dtype, "x")
+    _need(scale, shape[-1:], f32, "scale")
+    _need(dx, shape, dtype, "dx")
+    _need(dresidual, shape, rdtype, "dresidual")
+    sh = _norm_shape(dy, dtype, rdtype, 0.0)
+    one = scale is None and rdtype == dtype and (dx is None or dresidual is None)
+    if one:
+        dx = dresidual = dx if dx is not None else dresidual if dresidual is not None else _new(dy, shape, dtype)
+    else:
+        dx = _new(dy, shape, dtype) if dx is None else dx
+        dresidual = _new(dy, shape, rdtype) if dresidual is None else dresidual
+    dweight = _new(weight, weight.shape, f32)
+    dscale = None if scale is None else _new(scale, scale.shape, f32)
+    ref = ctypes.byref(sh)
+    workspace = _workspace(workspace, _query("ssd_norm_backward_workspace_size", ref), dy)
+    _launch(index, "ssd_add_rms_norm_backward", dy.data_ptr(), _p(dresidual_out), residual_out.data_ptr(),
+            weight.data_ptr(), rstd.data_ptr(), None if scale is None else x.data_ptr(), _p(scale), dx.data_ptr(),
+            None if one else dresidual.data_ptr(), dweight.data_ptr(), _p(dscale), ref, workspace.data_ptr(),
+            _bytes(workspace))
     return dx, dresidual, dweight, dscale
 
 
-def _gated_norm_inputs(x, z, weight, groups, eps, norm_before_gate):
-    torch = _torch()
-    D = x.shape[-1]
+def _gated_norm_shape(x, z, weight, groups, eps, norm_before_gate):
     _shaped(x, z.shape, x.dtype, "x")
-    _expect(weight, (D,), torch.float32, "weight")
-    sh = _norm_shape(math.prod(x.shape[:-1]), D, z.dtype, x.dtype, eps, groups, norm_before_gate)
-    sh.x_stride, sh.z_stride = _row_stride(x, "x"), _row_stride(z, "z")
-    return sh
+    _need(weight, x.shape[-1:], _torch().float32, "weight")
+    return _norm_shape(x, z.dtype, x.dtype, eps, groups, norm_before_gate, _row_stride(x, "x"), _row_stride(z, "z"))
 
 
 def gated_rms_norm(x, z, weight, *, groups: int = 1, eps: float = 1e-5, norm_before_gate: bool = False, y=None,
@@ -391,15 +408,14 @@ def gated_rms_norm(x, z, weight, *, groups: int = 1, eps: float = 1e-5, norm_bef
     x [..., D] in z's dtype or fp32, z [..., D] fp32 or bf16 (each may be a
     column range of a wider tensor), weight [D] fp32.  Returns y (z's dtype),
     or (y, rstd [..., groups] fp32) with ``want_rstd``."""
-    torch = _torch()
-    dev = _same_device(x, z, weight, y)
-    sh = _gated_norm_inputs(x, z, weight, groups, eps, norm_before_gate)
-    _expect(y, x.shape, z.dtype, "y")
-    with torch.cuda.device(dev):
-        y = _out(y, x.shape, z.dtype, "y", dev)
-        rstd = torch.empty(tuple(x.shape[:-1]) + (sh.groups,), dtype=torch.float32, device=dev) if want_rstd else None
-        _check(_lib().ssd_gated_rms_norm(x.data_ptr(), z.data_ptr(), _ptr(weight), _ptr(y), _ptr(rstd),
-                                         ctypes.byref(sh), _stream_handle(x)), "ssd_gated_rms_norm")
+    index = _gpu(x, z, weight, y)
+    sh = _gated_norm_shape(x, z, weight, groups, eps, norm_before_gate)
+    _need(y, x.shape, z.dtype, "y")
+    if y is None:
+        y = _new(x, x.shape, z.dtype)
+    rstd = _new(x, x.shape[:-1] + (groups,), _torch().float32) if want_rstd else None
+    _launch(index, "ssd_gated_rms_norm", x.data_ptr(), z.data_ptr(), weight.data_ptr(), y.data_ptr(), _p(rstd),
+            ctypes.byref(sh))
     return (y, rstd) if want_rstd else y
 
 
@@ -408,21 +424,24 @@ def gated_rms_norm_backward(dy, x, z, weight, rstd, *, groups: int = 1, norm_bef
     """Gradients of gated_rms_norm for dy (z's dtype) from its inputs and rstd:
     (dx, dz, dweight).  dx and dz may be given as column ranges of a wider
     tensor."""
-    torch = _torch()
-    dev = _same_device(x, z, dy, weight, rstd, dx, dz, workspace)
-    sh = _gated_norm_inputs(x, z, weight, groups, 0.0, norm_before_gate)
-    _expect(dy, x.shape, z.dtype, "dy")
-    _expect(rstd, tuple(x.shape[:-1]) + (sh.groups,), torch.float32, "rstd")
-    with torch.cuda.device(dev):
-        dx = _out(dx, x.shape, x.dtype, "dx", dev)
-        dz = _out(dz, x.shape, z.dtype, "dz", dev)
-        sh.dx_stride, sh.dz_stride = _row_stride(dx, "dx"), _row_stride(dz, "dz")
-        dweight = torch.empty(x.shape[-1], dtype=torch.float32, device=dev)
-        workspace = _norm_workspace(sh, workspace, dev)
-        _check(_lib().ssd_gated_rms_norm_backward(_ptr(dy), x.data_ptr(), z.data_ptr(), _ptr(weight), _ptr(rstd),
-                                                  dx.data_ptr(), dz.data_ptr(), _ptr(dweight), ctypes.byref(sh),
-                                                  _ptr(workspace), _bytes(workspace), _stream_handle(x)),
-               "ssd_gated_rms_norm_backward")
+    index = _gpu(x, z, dy, weight, rstd, dx, dz, workspace)
+    f32 = _torch().float32
+    sh = _gated_norm_shape(x, z, weight, groups, 0.0, norm_before_gate)
+    _need(dy, x.shape, z.dtype, "dy")
+    _need(rstd, x.shape[:-1] + (groups,), f32, "rstd")
+    if dx is None:
+        dx = _new(x, x.shape, x.dtype)
+    if dz is None:
+        dz = _new(x, x.shape, z.dtype)
+    _shaped(dx, x.shape, x.dtype, "dx")
+    _shaped(dz, x.shape, z.dtype, "dz")
+    sh.dx_stride, sh.dz_stride = _row_stride(dx, "dx"), _row_stride(dz, "dz")
+    dweight = _new(weight, weight.shape, f32)
+    ref = ctypes.byref(sh)
+    workspace = _workspace(workspace, _query("ssd_norm_backward_workspace_size", ref), x)
+    _launch(index, "ssd_gated_rms_norm_backward", dy.data_ptr(), x.data_ptr(), z.data_ptr(), weight.data_ptr(),
+            rstd.data_ptr(), dx.data_ptr(), dz.data_ptr(), dweight.data_ptr(), ref, workspace.data_ptr(),
+            _bytes(workspace))
     return dx, dz, dweight
 
 
@@ -437,41 +456,34 @@ def causal_conv1d_backward(dys, x, weight, bias=None, *, cu_seqlens=None, cu_seq
     Returns (dx, dweight [C, K] fp32, dbias [C] fp32 or None without a bias,
     dconv_state [b, K-1, C] or None); dconv_state is returned where conv_state
     is given, or as ``want_dstate`` says."""
-    torch = _torch()
     dys = list(dys)
-    if not dys:
-        raise ValueError("no output parts")
-    dev = _same_device(x, weight, bias, cu_seqlens, conv_state, dfinal_conv_state, dx, workspace, *dys)
-    C, K = x.shape[-1], weight.shape[-1]
-    _expect(x, x.shape, x.dtype, "x")
-    _expect(weight, (C, K), torch.float32, "weight")
-    _expect(bias, (C,), torch.float32, "bias")
+    if not 1 <= len(dys) <= 3:
+        raise ValueError("%d output parts, 1 to 3 are possible" % len(dys))
+    index = _gpu(x, weight, bias, cu_seqlens, conv_state, dfinal_conv_state, dx, workspace, *dys)
+    f32, (C, K) = _torch().float32, (x.shape[-1], weight.shape[-1])
+    _need(x, x.shape, x.dtype, "x")
+    _need(weight, (C, K), f32, "weight")
+    _need(bias, (C,), f32, "bias")
     sh = _ConvShape()
     keep = _sequences(sh, x, cu_seqlens, cu_seqlens_host)
-    n = sh.batch
-    _expect(conv_state, (n, K - 1, C), x.dtype, "conv_state")
-    _expect(dfinal_conv_state, (n, K - 1, C), x.dtype, "dfinal_conv_state")
-    _expect(dx, x.shape, x.dtype, "dx")
+    state = (sh.batch, K - 1, C)
+    _need(conv_state, state, x.dtype, "conv_state")
+    _need(dfinal_conv_state, state, x.dtype, "dfinal_conv_state")
+    _need(dx, x.shape, x.dtype, "dx")
     sh.channels, sh.width = C, K
-    sh.dtype, sh.ydtype = _dtype_code(x), _dtype_code_of(dys[0].dtype)
+    sh.dtype, sh.ydtype = _code(x.dtype), _code(dys[0].dtype)
     sh.activation = 1 if activation else 0
-    if len(dys) > 3:
-        raise ValueError("%d output parts, at most 3" % len(dys))
-    co, _ = _conv_outputs(x.shape[:-1], C, [t.shape[-1] for t in dys], dys, dys[0].dtype, dev)
-    lib = _lib()
-    with torch.cuda.device(dev):
-        dx = _out(dx, x.shape, x.dtype, "dx", dev)
-        dweight = torch.empty((C, K), dtype=torch.float32, device=dev)
-        dbias = None if bias is None else torch.empty(C, dtype=torch.float32, device=dev)
-        want = conv_state is not None if want_dstate is None else want_dstate
-        dstate = torch.empty((n, K - 1, C), dtype=x.dtype, device=dev) if want else None
-        need = ctypes.c_size_t(0)
-        _check(lib.ssd_causal_conv1d_backward_workspace_size(ctypes.byref(sh), ctypes.byref(need)),
-               "ssd_causal_conv1d_backward_workspace_size")
-        workspace = _workspace(workspace, need.value, dev)
-        _check(lib.ssd_causal_conv1d_backward(ctypes.byref(co), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_state),
-                                              _ptr(dfinal_conv_state), _ptr(dx), _ptr(dweight), _ptr(dbias),
-                                              _ptr(dstate), ctypes.byref(sh), _ptr(workspace), _bytes(workspace),
-                                              _stream_handle(x)), "ssd_causal_conv1d_backward")
+    parts, _ = _conv_outputs(x.shape[:-1], C, [t.shape[-1] for t in dys], dys, dys[0].dtype, x.device)
+    if dx is None:
+        dx = _new(x, x.shape, x.dtype)
+    dweight = _new(weight, weight.shape, f32)
+    dbias = None if bias is None else _new(bias, bias.shape, f32)
+    want = conv_state is not None if want_dstate is None else want_dstate
+    dstate = _new(x, state, x.dtype) if want else None
+    ref = ctypes.byref(sh)
+    workspace = _workspace(workspace, _query("ssd_causal_conv1d_backward_workspace_size", ref), x)
+    _launch(index, "ssd_causal_conv1d_backward", ctypes.byref(parts), x.data_ptr(), weight.data_ptr(), _p(bias),
+            _p(conv_state), _p(dfinal_conv_state), dx.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dstate), ref,
+            workspace.data_ptr(), _bytes(workspace))
     del keep
     return dx, dweight, dbias, dstate
