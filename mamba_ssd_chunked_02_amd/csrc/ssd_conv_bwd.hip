@@ -7,11 +7,12 @@
 // and what the final conv state's gradient adds to the last K-1 inputs.
 // About 6K + 12 operations per element: an HBM stream (x and dy in, dx out).
 //
-// A lane owns 4 consecutive channels and walks a block of rows in batches of
-// kBatch; the K-1 inputs and the K-1 dv around a batch stay in registers.
-// The rows just behind a block, whose dv its last dx need, are computed again
-// by the block behind (K-1 rows in block_rows).  A batch that touches no
-// sequence boundary takes a path with no test per row.
+// A lane owns 4 consecutive channels and walks a block of rows, sequence by
+// sequence, in batches of kBatch.  The K-1 inputs and the K-1 dv that a batch
+// shares with the next one stay in registers, and the next batch is in flight
+// while one is computed, so every row is loaded once; only the K-1 rows
+// behind a block, whose dv its last dx need, are loaded by two blocks.  A batch
+// inside its sequence and its block takes a path with no test per row.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,7 +23,7 @@ namespace ssd {
 namespace {
 
 constexpr int kBwdThreads = 256;
-constexpr int kBatch = 8;
+constexpr int kBatch = 4;
 constexpr int kCh = 4;
 constexpr int kWaveCh = 64 * kCh;
 
@@ -96,72 +97,98 @@ __global__ __launch_bounds__(kBwdThreads) void conv_backward_kernel(ConvBwdArgs 
     const T* xb = (const T*)a.x + c0;
     T* dxb = (T*)a.dx + c0;
     f32x4 dw[K] = {}, db = {};
+    typedef typename Raw<T>::type rawx;
+    typedef typename Raw<Y>::type rawy;
 
-    // One row by itself, for rows around a sequence boundary: its K inputs
-    // (from the state before its first token) and its dv.
-    struct Alone {
-        f32x4 h[K], dv;
-    };
-    auto alone = [&](int64_t t, int64_t s, RowRange q) {
-        Alone r;
-#pragma unroll
-        for (int k = 0; k < K; ++k) r.h[k] = padded_input<T, K>(a, s, q, t - q.lo + k, c0);
-        r.dv = dv_row<K, SILU>(tp, r.h, Tr<Y>::ld4(dyp.p + t * dyp.stride));
-        return r;
-    };
-
-    int64_t s = -1;
-    RowRange q = {0, 0};  // the sequence holding the current row
-    for (int64_t rb = r0; rb < r1; rb += kBatch) {
-        const int64_t re = min(rb + kBatch, r1);
-        if (rb >= q.hi && rb >= live.lo && rb < live.hi) {
-            s = seq_of(a.cu, a.nseq, a.L, rb);
-            q = seq_range(a.cu, a.L, a.T, s);
-        }
-        if (re - rb == kBatch && rb - (K - 1) >= q.lo && re + K - 1 <= q.hi) {
-            f32x4 h[kBatch + 2 * (K - 1)], dv[kBatch + K - 1];
-            typename Tr<Y>::v4 dy[kBatch + K - 1];
-#pragma unroll
-            for (int j = 0; j < kBatch + 2 * (K - 1); ++j) h[j] = Tr<T>::ld4(xb + (rb + j - (K - 1)) * a.C);
-#pragma unroll
-            for (int j = 0; j < kBatch + K - 1; ++j) dy[j] = Tr<Y>::ld4raw(dyp.p + (rb + j) * dyp.stride);
-#pragma unroll
-            for (int j = 0; j < kBatch + K - 1; ++j) dv[j] = dv_row<K, SILU>(tp, h + j, Tr<Y>::widen4(dy[j]));
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                f32x4 dx = {};
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    dx += tp.w[k] * dv[j + K - 1 - k];
-                    dw[k] += dv[j] * h[j + k];
-                }
-                db += dv[j];
-                if (on) Tr<T>::st4(dxb + (rb + j) * a.C, dx);
-            }
+    int64_t r = max(r0, live.lo);
+    const int64_t end = min(r1, live.hi);
+    while (r < end) {
+        const int64_t s = seq_of(a.cu, a.nseq, a.L, r);
+        const RowRange q = seq_range(a.cu, a.L, a.T, s);
+        if (r < q.lo || r >= q.hi) {  // an invalid offset list
+            ++r;
             continue;
         }
-        for (int64_t t = max(rb, live.lo); t < min(re, live.hi); ++t) {
-            if (t >= q.hi || t < q.lo) {
-                s = seq_of(a.cu, a.nseq, a.L, t);
-                q = seq_range(a.cu, a.L, a.T, s);
-                if (t < q.lo || t >= q.hi) continue;  // an invalid offset list
-            }
-            const Alone r = alone(t, s, q);
-            db += r.dv;
-            f32x4 dx = tp.w[K - 1] * r.dv;
+        const int64_t e = min(end, q.hi);  // this block's rows of the sequence: [r, e)
+        rawx xn[kBatch];
+        rawy yn[kBatch];
+        // rows t + K-1 .. of the batch at t; behind the last row the last one again, unused
+        auto load = [&](int64_t t) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) dw[k] += r.dv * r.h[k];
-            for (int d = 1; d < K && t + d < q.hi; ++d) {
-                const Alone n = alone(t + d, s, q);
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (k == K - 1 - d) dx += tp.w[k] * n.dv;
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t n = min(t + K - 1 + j, a.T - 1);
+                xn[j] = __builtin_nontemporal_load((const rawx*)(xb + n * a.C));
+                yn[j] = __builtin_nontemporal_load((const rawy*)(dyp.p + n * dyp.stride));
             }
-            // the final state holds the last K-1 inputs
-            if (a.dstate_out && t >= q.hi - (K - 1))
-                dx += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + t - (q.hi - (K - 1))) * a.C + c0);
-            if (on) Tr<T>::st4(dxb + t * a.C, dx);
+        };
+        load(r);
+        // the inputs and dv of the rows r .. r + K-2
+        f32x4 xh[K - 1], dvh[K - 1];
+        {
+            f32x4 in[2 * (K - 1)];
+#pragma unroll
+            for (int j = 0; j < 2 * (K - 1); ++j)
+                in[j] = r + j - (K - 1) < q.hi ? padded_input<T, K>(a, s, q, r - q.lo + j, c0) : f32x4{};
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                xh[j] = in[K - 1 + j];
+                dvh[j] = f32x4{};
+                if (r + j >= q.hi) continue;
+                dvh[j] = dv_row<K, SILU>(tp, in + j, Tr<Y>::ld4(dyp.p + (r + j) * dyp.stride));
+                if (r + j >= e) continue;
+                db += dvh[j];
+#pragma unroll
+                for (int k = 0; k < K; ++k) dw[k] += dvh[j] * in[j + k];
+            }
         }
+        // EDGE: the batch reaches the end of the block or of the sequence
+        auto batch = [&](int64_t t, auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
+            f32x4 h[K - 1 + kBatch], d[K - 1 + kBatch];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                h[j] = xh[j];
+                d[j] = dvh[j];
+            }
+            rawy y[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                h[K - 1 + j] = Raw<T>::widen(xn[j]);
+                y[j] = yn[j];
+            }
+            if (!EDGE) load(t + kBatch);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t n = t + K - 1 + j;
+                d[K - 1 + j] = f32x4{};
+                if (!EDGE || n < q.hi) {
+                    const f32x4 v = dv_row<K, SILU>(tp, h + j, Raw<Y>::widen(y[j]));
+                    d[K - 1 + j] = v;
+                    if (!EDGE || n < e) {
+                        db += v;
+#pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k] += v * h[j + k];
+                    }
+                }
+                if (EDGE && t + j >= e) continue;
+                f32x4 dx = {};
+#pragma unroll
+                for (int k = 0; k < K; ++k) dx += tp.w[k] * d[j + K - 1 - k];
+                // the final state holds the last K-1 inputs
+                if (EDGE && a.dstate_out && t + j >= q.hi - (K - 1))
+                    dx += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + t + j - (q.hi - (K - 1))) * a.C + c0);
+                if (on) __builtin_nontemporal_store(Tr<T>::narrow4(dx), (typename Tr<T>::v4*)(dxb + (t + j) * a.C));
+            }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                xh[j] = h[kBatch + j];
+                dvh[j] = d[kBatch + j];
+            }
+            if (EDGE) load(t + kBatch);
+        };
+        for (; r + kBatch + K - 1 <= e; r += kBatch) batch(r, std::false_type{});
+        for (; r < e; r += kBatch) batch(r, std::true_type{});
+        r = e;
     }
     // the workgroup's sums: waves 1..3 through LDS, added in order
     __shared__ f32x4 sums[3][K + 1][64];
