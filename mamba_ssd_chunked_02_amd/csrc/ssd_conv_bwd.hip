@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "ssd_column_sum.h"
 #include "ssd_gated.h"
 
 namespace ssd {
@@ -242,19 +243,12 @@ __global__ __launch_bounds__(kBwdThreads) void conv_backward_state_kernel(ConvBw
     }
 }
 
-// dweight [C, K] and dbias [C] from the workgroups' sums, in a fixed order:
-// 16 lanes a column take every 16th workgroup, then their sums are added.
+// dweight [C, K] and dbias [C] from the workgroups' sums.
 template <int K>
-__global__ __launch_bounds__(1024) void conv_backward_sum_kernel(ConvBwdArgs a, int64_t n) {
-    __shared__ float s_s[16][64];
-    const int l = threadIdx.x & 63, strip = threadIdx.x >> 6, c = blockIdx.x * 64 + l, k = blockIdx.y;
-    float s = 0.f;
-    if (c < a.C)
-        for (int64_t t = strip; t < n; t += 16) s += a.part[(t * (K + 1) + k) * a.C + c];
-    s_s[strip][l] = s;
-    __syncthreads();
-    if (strip || c >= a.C) return;
-    for (int j = 1; j < 16; ++j) s += s_s[j][l];
+__global__ __launch_bounds__(kSumThreads) void conv_backward_sum_kernel(ConvBwdArgs a, int64_t n) {
+    const int c = blockIdx.x * kSumCols + threadIdx.x % kSumCols, k = blockIdx.y;
+    const float s = column_sum(n, [&](int64_t t) { return c < a.C ? a.part[(t * (K + 1) + k) * a.C + c] : 0.f; });
+    if (threadIdx.x >= kSumCols || c >= a.C) return;
     if (k < K) a.dweight[(int64_t)c * K + k] = s;
     else if (a.dbias) a.dbias[c] = s;
 }
@@ -268,7 +262,8 @@ hipError_t run_conv_backward(const ConvBwdArgs& a, hipStream_t stream) {
                            stream, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((conv_backward_sum_kernel<K>), dim3((unsigned)((a.C + 63) / 64), K + 1), dim3(1024), 0, stream, a,
+    hipLaunchKernelGGL((conv_backward_sum_kernel<K>), dim3((unsigned)((a.C + kSumCols - 1) / kSumCols), K + 1),
+                       dim3(kSumThreads), 0, stream, a,
                        (int64_t)(a.T > 0 ? a.nblocks : 0));
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.dstate_in && a.nseq > 0) {

@@ -73,8 +73,26 @@ __device__ inline float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
 }
 
-// log(1 + exp(v)) in fp32 without cancellation on either side.
-__device__ inline float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+// softplus(v) = max(v, 0) + log(1 + u), u = exp(-|v|) <= 1, to about 4 of 2^-24.
+// u: the product with log2(e) in two parts, the small one to first order;
+// log(1 + u) = 2 atanh(s), s = u / (2 + u) <= 1/3: the series to s^13 (the first
+// term left out is below 2^-25 of it).  Below -87, where u is no normal number, 0.
+// 25 operations; expf and log1pf take four
+// times as many, which the single-token step would wait for.
+__device__ inline float softplus_f(float v) {
+    const float n0 = -fabsf(v), n = n0 < -88.f ? -88.f : n0, t = n * 0x1.715476p+0f;  // NaN stays
+    const float lo = __builtin_fmaf(n, 0x1.715476p+0f, -t) + n * 0x1.4ae0cp-26f;
+    const float u0 = __builtin_amdgcn_exp2f(t), u = __builtin_fmaf(u0, lo * 0x1.62e43p-1f, u0);
+    const float s = u * __builtin_amdgcn_rcpf(2.f + u), q = s * s;
+    float p = 2.f / 13.f;
+    p = __builtin_fmaf(p, q, 2.f / 11.f);
+    p = __builtin_fmaf(p, q, 2.f / 9.f);
+    p = __builtin_fmaf(p, q, 2.f / 7.f);
+    p = __builtin_fmaf(p, q, 2.f / 5.f);
+    p = __builtin_fmaf(p, q, 2.f / 3.f);
+    p = __builtin_fmaf(p, q, 2.f);
+    return v < -87.f ? 0.f : fmaxf(v, 0.f) + s * p;
+}
 
 // The factor of sigmoid(r) in log a: -rate softplus(lam), no lower than -1e4
 // (exp of which is 0) so that sums of it stay finite; NaN stays NaN.

@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "ssd_column_sum.h"
 #include "ssd_gated.h"
 
 namespace ssd {
@@ -567,18 +568,12 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
     }
 }
 
-// dlam from the tiles' sums, in a fixed order: 16 lanes a channel take every
-// 16th tile, then their sums are added.
-__global__ __launch_bounds__(1024) void gated_dlam_kernel(GatedArgs a, int64_t ntiles, const float* part, float* dlam) {
-    __shared__ float s_s[16][64];
-    const int c = threadIdx.x & 63, strip = threadIdx.x >> 6, ch = blockIdx.x * 64 + c;
-    float s = 0.f;
-    if (ch < a.C)
-        for (int64_t t = strip; t < ntiles; t += 16) s += part[t * a.C + ch];
-    s_s[strip][c] = s;
-    __syncthreads();
-    if (strip || ch >= a.C) return;
-    for (int j = 1; j < 16; ++j) s += s_s[j][c];
+// dlam from the tiles' sums.
+__global__ __launch_bounds__(kSumThreads) void gated_dlam_kernel(GatedArgs a, int64_t ntiles, const float* part,
+                                                                 float* dlam) {
+    const int ch = blockIdx.x * kSumCols + threadIdx.x % kSumCols;
+    const float s = column_sum(ntiles, [&](int64_t t) { return ch < a.C ? part[t * a.C + ch] : 0.f; });
+    if (threadIdx.x >= kSumCols || ch >= a.C) return;
     // sigmoid(lam) / softplus(lam): 1 towards minus infinity, where both vanish
     const float lam = a.lam[ch], sp = softplus_f(lam);
     dlam[ch] = s * (sp < 1e-30f ? 1.f : (1.f / (1.f + expf(-lam))) / sp);
@@ -649,7 +644,7 @@ hipError_t run_backward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream
                            dim3(kTileRows / kBwdRows * kSegLanes), 0, stream, a, ps, part);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(gated_dlam_kernel, dim3(blocks_of(a.C, 64)), dim3(1024), 0, stream, a, lay.ntiles,
+    hipLaunchKernelGGL(gated_dlam_kernel, dim3(blocks_of(a.C, kSumCols)), dim3(kSumThreads), 0, stream, a, lay.ntiles,
                        (const float*)part, a.dlam);
     return hipGetLastError();
 }

@@ -12,6 +12,7 @@
 // 8 consecutive columns at a time.
 #include <algorithm>
 
+#include "ssd_column_sum.h"
 #include "ssd_device.h"
 
 namespace ssd {
@@ -214,19 +215,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(NormArgs a)
     }
 }
 
-// 64 columns a workgroup: 16 lanes a column take every 16th row, then their
-// sums are added in order.
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int64_t n, int64_t ld, int cols, float* out) {
-    __shared__ float s_s[16][64];
-    const int c = threadIdx.x & 63, strip = threadIdx.x >> 6, col = blockIdx.x * 64 + c;
-    float s = 0.f;
-    if (col < cols)
-        for (int64_t t = strip; t < n; t += 16) s += part[t * ld + col];
-    s_s[strip][c] = s;
-    __syncthreads();
-    if (strip || col >= cols) return;
-    for (int j = 1; j < 16; ++j) s += s_s[j][c];
-    out[col] = s;
+__global__ __launch_bounds__(kSumThreads) void column_sum_kernel(const float* part, int64_t n, int64_t ld, int cols,
+                                                                 float* out) {
+    const int col = blockIdx.x * kSumCols + threadIdx.x % kSumCols;
+    const float s = column_sum(n, [&](int64_t t) { return col < cols ? part[t * ld + col] : 0.f; });
+    if (threadIdx.x < kSumCols && col < cols) out[col] = s;
 }
 
 template <typename A, typename B, int KIND, int WPR, int V>
@@ -297,7 +290,7 @@ hipError_t launch_gated_norm_backward(const NormArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_column_sum(const float* part, int64_t n, int64_t ld, int32_t cols, float* out, hipStream_t stream) {
-    hipLaunchKernelGGL(column_sum_kernel, dim3((cols + 63) / 64), dim3(1024), 0, stream, part, n, ld, cols, out);
+    hipLaunchKernelGGL(column_sum_kernel, dim3((cols + kSumCols - 1) / kSumCols), dim3(kSumThreads), 0, stream, part, n, ld, cols, out);
     return hipGetLastError();
 }
 

@@ -7,7 +7,7 @@ graphs, and a prefill continued by steps.
 
 Error counts, in units of 2^-24 of the scale (sums of absolute values):
   sigmoid(v), |v| <= 6   exp2's argument 2|v|, exp2 2, add 1, reciprocal 2: <= 17
-  log a                  softplus and the factor 6 more: 23 of itself, so at most
+  log a                  softplus (4) and the factor 6 more: 23 of itself, so at most
                          23 |S| exp(-|S|) <= 9 in a product of a over any run
   the recurrence         a's rounding and one more a row of a run of rows: 16; b: 17 + 12 + 4
   a run's factor P       its sum, exp2 and their product with the state: 16 a run,
