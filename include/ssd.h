@@ -446,10 +446,10 @@ typedef struct ssd_gated_shape {
 
 /*
  * Rows of the saved states: the forward pass can keep the fp32 state entering
- * every SSD_GATED_TILE_ROWS rows of the batch's rows, [states_rows, C] with
- * states_rows = ceil(rows / SSD_GATED_TILE_ROWS); the backward pass needs it.
+ * every SSD_GATED_STATE_ROWS rows of the batch's rows, [states_rows, C] with
+ * states_rows = ceil(rows / SSD_GATED_STATE_ROWS); the backward pass needs it.
  */
-#define SSD_GATED_TILE_ROWS 128
+#define SSD_GATED_STATE_ROWS 64
 
 /* Workspace bytes of ssd_gated_scan (backward = 0) or _backward (1). */
 ssd_status ssd_gated_scan_workspace_size(const ssd_gated_shape* shape, int32_t backward, size_t* bytes);

@@ -21,9 +21,9 @@ from typing import Optional, Sequence
 from . import (SSD_BF16, SSD_F32, SsdError, _conv_outputs, _ConvShape, _dtype_code_of, _expect, _torch, load)
 
 __all__ = ["gated_scan", "gated_scan_step", "gated_scan_backward", "add_rms_norm", "add_rms_norm_backward",
-           "gated_rms_norm", "gated_rms_norm_backward", "causal_conv1d_backward", "GATED_TILE_ROWS"]
+           "gated_rms_norm", "gated_rms_norm_backward", "causal_conv1d_backward", "GATED_STATE_ROWS"]
 
-GATED_TILE_ROWS = 128  # SSD_GATED_TILE_ROWS of include/ssd.h
+GATED_STATE_ROWS = 64  # SSD_GATED_STATE_ROWS of include/ssd.h
 
 
 class _GatedShape(ctypes.Structure):
@@ -223,7 +223,7 @@ def gated_scan(x, r, i, lam, *, rate: float = 8.0, init_state=None, cu_seqlens=N
     Returns (y, final_state), y of x's dtype unless ``y_dtype`` says fp32 or
     bf16, final_state [b, C] fp32 (None with ``want_final=False``); with
     ``want_states`` (y, final_state, states), the fp32 states that
-    gated_scan_backward needs, [ceil(rows / GATED_TILE_ROWS), C].
+    gated_scan_backward needs, [ceil(rows / GATED_STATE_ROWS), C].
 
     A sequence of no tokens passes its state through.  Rows behind the last
     sequence of a packed batch are left as they were in y."""
@@ -251,7 +251,7 @@ def gated_scan(x, r, i, lam, *, rate: float = 8.0, init_state=None, cu_seqlens=N
 
 
 def _states_shape(x):
-    return -(-math.prod(x.shape[:-1]) // GATED_TILE_ROWS), x.shape[-1]
+    return -(-math.prod(x.shape[:-1]) // GATED_STATE_ROWS), x.shape[-1]
 
 
 def gated_scan_backward(dy, x, r, i, lam, states, *, rate: float = 8.0, init_state=None, dfinal_state=None,

@@ -5,7 +5,7 @@
 // and its gradients.  About 40 fp32 operations (6 of them quarter rate) and 8
 // bytes (bf16) an element: an HBM stream, with the vector ALU close behind.
 //
-// The token axis of the whole batch is cut into tiles of kTileRows rows
+// The token axis of the whole batch is cut into tiles of 128 rows (64 backward)
 // whatever the sequences' lengths; a sequence start inside a tile resets the
 // state there.  A step is the map h -> a h + b, and a run of steps is again
 // such a map (P, H): state at the end = P * (state before) + H.  A reset in a
@@ -15,10 +15,10 @@
 //
 // One pass over the data: a workgroup holds its tile in registers, publishes
 // the tile's map, folds the maps of the tiles before it into the state that
-// enters its own, and finishes.  Tiles go in groups of 16: a tile folds the maps
+// enters its own, and finishes.  Tiles go in groups of 8: a tile folds the maps
 // of its group's earlier tiles, in order, onto the state entering the group,
 // which the last tile of the group before publishes.  So the order of every sum
-// is fixed, and only one step in 16 tiles is a chain.
+// is fixed, and only one step in 8 tiles is a chain.
 //   Why the waits end: the tiles of a channel block are handed out in order by
 // a counter, so every tile that a workgroup waits for belongs to a workgroup
 // that runs already, and a tile's map is published before its workgroup waits
@@ -41,10 +41,10 @@ namespace {
 constexpr int kLaneCh = 4;                      // channels per lane
 constexpr int kSegLanes = 16;                   // lanes across the channels of a row
 constexpr int kTileCh = kLaneCh * kSegLanes;    // channels per workgroup
-constexpr int kTileRows = kGatedTileRows;
-constexpr int kGroup = 16;                      // tiles per group of the carry
+constexpr int kFwdTile = 128, kBwdTile = kGatedStateRows;  // rows per tile
+constexpr int kGroup = 8;                       // tiles per group of the carry
 constexpr int kBitRows = 8;                     // rows per word of boundary bits
-constexpr int kFwdRows = 8, kBwdRows = 8;       // rows per run (per lane)
+constexpr int kFwdRows = 8, kBwdRows = 4;       // rows per run (per lane)
 constexpr uint64_t kNotYet = ~(uint64_t)0;      // a published word that is not there yet
 
 __device__ inline bool is_reset(float P) { return __builtin_bit_cast(int, P) < 0; }
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, GatedPlan 
 // What a lane has of its run of rows: the place, the boundary bits and the
 // live rows (bit j).  plain: no run of the wave has a boundary or a row that is
 // not live, and so none of the tests per row is needed.
-template <int ROWS>
+template <int ROWS, int TILE>
 struct Run {
     int64_t tile0;   // the tile's first row
     int row;         // the run's first row in the tile
@@ -145,7 +145,7 @@ struct Run {
     __device__ bool any_end() const { return bits >> 16 & live; }
 
     __device__ Run(const GatedArgs& a, int64_t tile, int cb) {
-        tile0 = tile * kTileRows;
+        tile0 = tile * TILE;
         row = (int)(threadIdx.x / kSegLanes) * ROWS;
         const int c = cb * kTileCh + (threadIdx.x % kSegLanes) * kLaneCh;
         on = c < a.C;
@@ -153,7 +153,7 @@ struct Run {
         if (!a.cu) {
             // rows < 2^31; the whole tile between two boundaries, or not
             const uint32_t p = (uint32_t)tile0 % (uint32_t)a.L;
-            if (p && a.L - p > kTileRows) {
+            if (p && a.L - p > TILE) {
                 bits = 0;
                 live = (1u << ROWS) - 1;
                 plain = 1;
@@ -179,12 +179,12 @@ __device__ inline T* at_row(T* p, int64_t row0, int64_t stride, uint32_t bytes) 
 
 // The data is read once and written once: streaming loads and stores.  A tile
 // that reaches past the last row reads that row instead.
-template <typename T, int ROWS>
-__device__ inline void load_rows(const GatedArgs& a, const Run<ROWS>& u, const void* p, int64_t stride,
+template <typename T, int ROWS, int TILE>
+__device__ inline void load_rows(const GatedArgs& a, const Run<ROWS, TILE>& u, const void* p, int64_t stride,
                                  typename Raw<T>::type (&v)[ROWS]) {
     typedef typename Raw<T>::type raw;
     T* const q = (T*)const_cast<void*>(p);
-    if (u.tile0 + kTileRows <= a.T) {
+    if (u.tile0 + TILE <= a.T) {
         const uint32_t bytes = ((uint32_t)u.row * (uint32_t)stride + (uint32_t)u.c0) * sizeof(T);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) v[j] = __builtin_nontemporal_load((const raw*)at_row(q, u.tile0 + j, stride, bytes));
@@ -197,8 +197,8 @@ __device__ inline void load_rows(const GatedArgs& a, const Run<ROWS>& u, const v
     }
 }
 
-template <typename T, int ROWS>
-__device__ inline void store_row(const Run<ROWS>& u, void* p, int64_t stride, int j, f32x4 v) {
+template <typename T, int ROWS, int TILE>
+__device__ inline void store_row(const Run<ROWS, TILE>& u, void* p, int64_t stride, int j, f32x4 v) {
     const uint32_t bytes = ((uint32_t)u.row * (uint32_t)stride + (uint32_t)u.c0) * sizeof(T);
     __builtin_nontemporal_store(Tr<T>::narrow4(v), (typename Tr<T>::v4*)at_row((T*)p, u.tile0 + j, stride, bytes));
 }
@@ -208,8 +208,8 @@ __device__ inline int64_t state_at(const GatedArgs& a, int64_t row, int c0) {
 }
 
 // Rows that are not live become steps that change nothing: log a = 0, x = 0.
-template <typename T, int ROWS>
-__device__ inline void idle_rows(const Run<ROWS>& u, typename Raw<T>::type (&xv)[ROWS], typename Raw<T>::type (&rv)[ROWS],
+template <typename T, int ROWS, int TILE>
+__device__ inline void idle_rows(const Run<ROWS, TILE>& u, typename Raw<T>::type (&xv)[ROWS], typename Raw<T>::type (&rv)[ROWS],
                                  typename Raw<T>::type (&iv)[ROWS]) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j)
@@ -226,10 +226,11 @@ __device__ inline f32x4 seq_state(const GatedArgs& a, const float* st, int64_t r
 // The value is computed here and kept, and what it was computed from is
 // forgotten: without this the compiler keeps every row's intermediate values
 // alive for a later use of the same expression, 40 to 90 registers more.
-__device__ inline void pin(f32x4& v) {
+template <typename V>
+__device__ inline void pin(V& v) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float t = v[c];
+    for (int c = 0; c < (int)(sizeof(V) / 4); ++c) {
+        auto t = v[c];
         asm volatile("" : "+v"(t));
         v[c] = t;
     }
@@ -257,8 +258,8 @@ struct Step {
 
 // At a sequence's first row the initial state goes into b and the state before
 // it counts as 0: H goes on from (a, b) of row j.
-template <int ROWS>
-__device__ inline void take_row(const GatedArgs& a, const Run<ROWS>& u, int j, f32x4 av, f32x4& b, f32x4& H) {
+template <int ROWS, int TILE>
+__device__ inline void take_row(const GatedArgs& a, const Run<ROWS, TILE>& u, int j, f32x4 av, f32x4& b, f32x4& H) {
     if (!u.plain)
         if (u.start(j)) {
             b += av * seq_state(a, a.init, u.t(j), u.c0);
@@ -298,7 +299,7 @@ struct Fold {
     __device__ void map(int ch, float& Pt, float& Ht) const {
         Pt = 1.f;
         Ht = 0.f;
-#pragma unroll 8
+#pragma unroll 4
         for (int s = 0; s < RUNS; ++s) {
             const float p = P[at(s) + ch];
             Ht = advance(p, H[at(s) + ch], Ht);
@@ -307,8 +308,14 @@ struct Fold {
     }
     // H replaced by the state entering each run
     __device__ void enter(int ch, float h) const {
-#pragma unroll 8
+        enter(ch, h, [](int, float) {});
+    }
+    // seen(s, h): run s is entered with h
+    template <typename F>
+    __device__ void enter(int ch, float h, F seen) const {
+#pragma unroll 4
         for (int s = 0; s < RUNS; ++s) {
+            seen(s, h);
             float* const to = const_cast<float*>(H) + at(s) + ch;
             const float n = advance(P[at(s) + ch], *to, h);
             *to = h;
@@ -317,22 +324,30 @@ struct Fold {
     }
 };
 
+// The tile's own map, for the later tiles of its group (by wave 0; the last
+// tile's goes into the state entering the next group instead).
+__device__ inline void publish_map(const GatedPass& ps, int64_t ord, int chan, int C, float Pt, float Ht) {
+    if (chan < C && ord % kGroup < kGroup - 1 && ord + 1 < ps.ntiles) publish(ps.maps + ord * C + chan, Pt, Ht);
+}
+
 // The state entering tile `ord` (counted in the pass's order) for channel
-// ch of the workgroup, valid in wave 0.  (Pt, Ht): the tile's own map, in wave 0.
-// Every wave calls it; group_s: [kGroup][kTileCh] pairs.
+// chan = channel block * 64 + lane, valid in wave 0.  (Pt, Ht): the tile's own
+// map, in wave 0.  Every wave calls it; group_s: [kGroup][kTileCh] pairs.
 template <int WAVES>
 __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, int C, float Pt, float Ht, f32x2* group_s) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool on = chan < C;
+    const int at = on ? chan : 0;
     const int p = (int)(ord % kGroup);
     const int64_t g = ord / kGroup;
-    if (wave == 0 && on && p < kGroup - 1 && ord + 1 < ps.ntiles) publish(ps.maps + ord * C + chan, Pt, Ht);
+    // wave 0 asks for the group's entry along with the maps
+    uint64_t e = wave == 0 && g > 0 ? look(ps.entry + g * C + at) : 0;
     // the maps of the group's earlier tiles: wave w takes kGroup / WAVES of them
     constexpr int kEach = kGroup / WAVES;
-    uint64_t v[kEach];
     const int j0 = wave * kEach;
     if (j0 < p) {
-        const uint64_t* m = ps.maps + (g * kGroup + j0) * C + (on ? chan : 0);
+        const uint64_t* m = ps.maps + (g * kGroup + j0) * C + at;
+        uint64_t v[kEach];
         while (true) {
             bool ready = true;
 #pragma unroll
@@ -354,13 +369,11 @@ __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, i
         h = advance(m[0], m[1], h);
         Pp = chain(Pp, m[0]);
     }
+    // a sequence that starts in the group needs nothing from before it
     if (g > 0 && !__all(is_reset(Pp))) {
-        const uint64_t* c = ps.entry + g * C + (on ? chan : 0);
-        uint64_t e;
-        while (true) {
-            e = look(c);
-            if (__all(there(e))) break;
+        while (!__all(there(e))) {
             __builtin_amdgcn_s_sleep(1);
+            e = look(ps.entry + g * C + at);
         }
         h = advance(Pp, h, lo_of(e));
     }
@@ -370,8 +383,8 @@ __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, i
 
 // ------------------------------------------------------------------ forward
 template <typename T, typename Y>
-__global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forward_kernel(GatedArgs a, GatedPass ps) {
-    constexpr int R = kFwdRows, kRuns = kTileRows / R;
+__global__ __launch_bounds__(kFwdTile / kFwdRows * kSegLanes) void gated_forward_kernel(GatedArgs a, GatedPass ps) {
+    constexpr int R = kFwdRows, kRuns = kFwdTile / R;
     __shared__ uint32_t slot;
     __shared__ float k_s[kTileCh];
     __shared__ f32x4 P_s[kRuns][kSegLanes], H_s[kRuns][kSegLanes];
@@ -381,7 +394,7 @@ __global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forwar
     if (threadIdx.x < kTileCh)
         k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
     const int64_t tile = next_tile(ps, cb, &slot);
-    const Run<R> u(a, tile, cb);
+    const Run<R, kFwdTile> u(a, tile, cb);
     typename Raw<T>::type xv[R], rv[R], iv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
     load_rows<T>(a, u, a.i, a.i_stride, iv);
@@ -411,12 +424,20 @@ __global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forwar
     const int ch = threadIdx.x & 63, chan = cb * kTileCh + ch;
     float Pt = 1.f, Ht = 0.f, h0 = 0.f;
     if (ps.counters) {
-        if (threadIdx.x < kTileCh) fold.map(ch, Pt, Ht);
+        if (threadIdx.x < kTileCh) {
+            fold.map(ch, Pt, Ht);
+            publish_map(ps, tile, chan, a.C, Pt, Ht);
+        }
         h0 = enter_tile<kRuns / 4>(ps, tile, chan, a.C, Pt, Ht, group_s);
     }
     if (threadIdx.x < kTileCh) {
-        if (a.states_out && chan < a.C) a.states_out[tile * a.C + chan] = h0;
-        fold.enter(ch, h0);
+        constexpr int kEvery = kGatedStateRows / R, kHere = kFwdTile / kGatedStateRows;
+        if (a.states_out && chan < a.C)
+            fold.enter(ch, h0, [&](int s, float h) {
+                const int64_t at = tile * kHere + s / kEvery;
+                if (s % kEvery == 0 && at * kGatedStateRows < a.T) a.states_out[at * a.C + chan] = h;
+            });
+        else fold.enter(ch, h0);
     }
     __syncthreads();
     if (!u.on) return;
@@ -444,9 +465,9 @@ __global__ __launch_bounds__(kTileRows / kFwdRows * kSegLanes) void gated_forwar
 // h_{t-1} is recomputed in fp32 from the state entering the tile, which the
 // forward pass kept; the adjoint is carried over the tiles in reverse order.
 template <typename T, typename Y>
-__global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backward_kernel(GatedArgs a, GatedPass ps,
+__global__ __launch_bounds__(kBwdTile / kBwdRows * kSegLanes, sizeof(T) == 2 ? 4 : 3) void gated_backward_kernel(GatedArgs a, GatedPass ps,
                                                                                           float* dlam_part) {
-    constexpr int R = kBwdRows, kRuns = kTileRows / R;
+    constexpr int R = kBwdRows, kRuns = kBwdTile / R;
     __shared__ uint32_t slot;
     __shared__ float k_s[kTileCh];
     __shared__ f32x4 P_s[kRuns][kSegLanes], H_s[kRuns][kSegLanes], R_s[kRuns][kSegLanes], Q_s[kRuns][kSegLanes];
@@ -456,7 +477,7 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
     if (threadIdx.x < kTileCh)
         k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
     const int64_t ord = next_tile(ps, cb, &slot), tile = ps.ntiles - 1 - ord;
-    const Run<R> u(a, tile, cb);
+    const Run<R, kBwdTile> u(a, tile, cb);
     typename Raw<T>::type xv[R], rv[R], iv[R];
     typename Raw<Y>::type dv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
@@ -470,20 +491,19 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
     const f32x4 k = *(const f32x4*)(k_s + ln * kLaneCh);
     const int slow = slow_wave(k);
     if (!u.plain) idle_rows<T>(u, xv, rv, iv);
+    // first what the adjoint's map needs: the decays and dy
     f32x4 w[R], b[R], sr[R], si[R], S = {}, H = {}, Q = {};
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        const Step<T> st(k, slow, xv[j], rv[j], iv[j]);
-        S += st.sr;
-        sr[j] = st.sr;
-        si[j] = st.si;
-        w[j] = st.w;
-        b[j] = st.b;
-        take_row(a, u, j, st.a, b[j], H);
+        const f32x4 r = Raw<T>::widen(rv[j]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sr[j][c] = sigmoid_f(r[c]);
+        S += sr[j];
+        Decay d;
+        d.from_log(k * sr[j], slow);
+        w[j] = d.w;
         pin(sr[j]);
-        pin(si[j]);
         pin(w[j]);
-        pin(b[j]);
         pin(S);
     }
     S *= k;
@@ -496,20 +516,40 @@ __global__ __launch_bounds__(kTileRows / kBwdRows * kSegLanes) void gated_backwa
         }
         Q = decay_of(w[j], slow) * (Q + g);
         pin(w[j]);
+        pin(dv[j]);
     }
-    P_s[seg][ln] = run_factor(S, u.any_start());
-    H_s[seg][ln] = H;
     R_s[seg][ln] = run_factor(S, u.any_end());
     Q_s[seg][ln] = Q;
     __syncthreads();
     const Fold<kRuns, false> states{(const float*)P_s, (const float*)H_s};
     const Fold<kRuns, true> adjoints{(const float*)R_s, (const float*)Q_s};
-    if (threadIdx.x >> 6 == 1) states.enter(ch, state0);
     float Rt = 1.f, Qt = 0.f, q0 = 0.f;
-    if (ps.counters) {
-        if (threadIdx.x < kTileCh) adjoints.map(ch, Rt, Qt);
-        q0 = enter_tile<kRuns / 4>(ps, ord, chan, a.C, Rt, Qt, group_s);
+    if (ps.counters && threadIdx.x < kTileCh) {
+        adjoints.map(ch, Rt, Qt);
+        publish_map(ps, ord, chan, a.C, Rt, Qt);
     }
+    // then the states, while the earlier tiles' maps arrive
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const f32x4 x = Raw<T>::widen(xv[j]), i = Raw<T>::widen(iv[j]);
+        Decay d;
+        d.from_held(w[j], slow);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            si[j][c] = sigmoid_f(i[c]);
+            b[j][c] = __builtin_amdgcn_sqrtf(d.m[c]) * si[j][c] * x[c];
+        }
+        take_row(a, u, j, d.a, b[j], H);
+        pin(si[j]);
+        pin(b[j]);
+        pin(w[j]);
+        pin(xv[j]);
+    }
+    P_s[seg][ln] = run_factor(S, u.any_start());
+    H_s[seg][ln] = H;
+    __syncthreads();
+    if (threadIdx.x >> 6 == 1) states.enter(ch, state0);
+    if (ps.counters) q0 = enter_tile<kRuns / 4>(ps, ord, chan, a.C, Rt, Qt, group_s);
     if (threadIdx.x < kTileCh) adjoints.enter(ch, q0);
     __syncthreads();
 
@@ -629,7 +669,7 @@ hipError_t run_forward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream_
     const hipError_t e = run_plan(a, lay, ws, a.init, a.final_state, &ps, stream);
     if (e != hipSuccess || a.T == 0) return e;
     hipLaunchKernelGGL((gated_forward_kernel<T, Y>), dim3((unsigned)(lay.ntiles * ps.nblocks)),
-                       dim3(kTileRows / kFwdRows * kSegLanes), 0, stream, a, ps);
+                       dim3(kFwdTile / kFwdRows * kSegLanes), 0, stream, a, ps);
     return hipGetLastError();
 }
 
@@ -641,7 +681,7 @@ hipError_t run_backward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream
     float* part = (float*)(ws + lay.dlam);
     if (a.T > 0) {
         hipLaunchKernelGGL((gated_backward_kernel<T, Y>), dim3((unsigned)(lay.ntiles * ps.nblocks)),
-                           dim3(kTileRows / kBwdRows * kSegLanes), 0, stream, a, ps, part);
+                           dim3(kBwdTile / kBwdRows * kSegLanes), 0, stream, a, ps, part);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     hipLaunchKernelGGL(gated_dlam_kernel, dim3(blocks_of(a.C, kSumCols)), dim3(kSumThreads), 0, stream, a, lay.ntiles,
@@ -661,7 +701,8 @@ hipError_t run_gated_step(const GatedArgs& a, const float* state, float* state_o
 
 GatedLayout gated_layout(int64_t T, int32_t C, bool packed, bool backward) {
     GatedLayout l;
-    l.ntiles = (T + kTileRows - 1) / kTileRows;
+    const int rows = backward ? kBwdTile : kFwdTile;
+    l.ntiles = (T + rows - 1) / rows;
     l.ngroups = (l.ntiles + kGroup - 1) / kGroup;
     size_t at = 0;
     auto take = [&](size_t bytes) {

@@ -182,9 +182,9 @@ struct ConvArgs {
     int32_t dtype, y_f32, silu;
 };
 
-// Gated linear recurrence (ssd_gated.hip): the tokens of the whole batch are
-// cut into tiles of this many rows.
-constexpr int kGatedTileRows = 128;
+// Gated linear recurrence (ssd_gated.hip): the forward pass can keep the state
+// entering every so many rows, which the backward pass starts its tiles from.
+constexpr int kGatedStateRows = 64;
 
 struct GatedArgs {
     const void* x;             // [rows, C] with row stride x_stride (elements)
@@ -201,7 +201,7 @@ struct GatedArgs {
     float rate;
     void* y;                   // [rows, C]
     float* final_state;        // [nseq, C] or NULL
-    float* states_out;         // [ntiles, C] or NULL: the state entering every tile
+    float* states_out;         // [ceil(T / kGatedStateRows), C] or NULL: the states entering those rows
     // backward
     const void* dy;            // [rows, C]
     const float* states_in;    // states_out of the forward pass

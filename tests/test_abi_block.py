@@ -192,8 +192,8 @@ def test_conv_backward_refusals(lib):
 
 
 def test_binding_constants_and_refusals():
-    m = re.search(r"#define SSD_GATED_TILE_ROWS (\d+)", open(HEADER).read())
-    assert m and int(m.group(1)) == ops.GATED_TILE_ROWS
+    m = re.search(r"#define SSD_GATED_STATE_ROWS (\d+)", open(HEADER).read())
+    assert m and int(m.group(1)) == ops.GATED_STATE_ROWS
     x, lam = torch.zeros(1, 4, 8), torch.zeros(8)
     with pytest.raises(ValueError):
         ssd.gated_scan(x, x, x, lam)
