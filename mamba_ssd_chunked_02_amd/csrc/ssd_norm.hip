@@ -7,10 +7,14 @@
 // A few operations per element read: HBM streams.  A row is held in
 // registers between the sum and its use, so every input is read once.
 //
-// A row of up to 4096 columns is one wave's (no LDS, no barrier: the four
-// waves of a workgroup run apart), a longer one a workgroup's.  A lane takes
-// 8 consecutive columns at a time.
+// A row (or group of a row) belongs to a team of lanes, 8 consecutive columns
+// each: 8 to 64 lanes of a wave, or all waves of a workgroup where it is wider.
+// Wide rows over many waves with few registers a lane beat one wave with many
+// (65536 rows of 2560 columns, forward and backward: 5 waves a row and the
+// next row in flight 974 us, one wave a row 1069 us; 256 rows forward 4.2
+// against 5.8 us), and narrow groups share a wave.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssd_column_sum.h"
 #include "ssd_device.h"
@@ -19,42 +23,53 @@ namespace ssd {
 
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr int kVec = 8;
+constexpr int kMaxWaves = 8;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Eight consecutive elements as loaded.  The data is read and written once:
+// bf16, 16 bytes a lane and whole lines a wave, streams past the caches
+// (49152 rows of 8192 columns forward and backward 1159 us, cached 1180 us);
+// fp32 takes two accesses that share every line and needs the cache between
+// them (974 us cached, 1037 us streamed).
+template <typename T>
+struct Eight;
+template <>
+struct Eight<bf16_t> {
+    typedef u32x4 raw;
+    __device__ static inline raw load(const bf16_t* p) { return __builtin_nontemporal_load((const raw*)p); }
+    __device__ static inline f32x8 widen(raw v) {
+        f32x8 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[2 * e] = __builtin_bit_cast(float, v[e] << 16);
+            r[2 * e + 1] = __builtin_bit_cast(float, v[e] & 0xffff0000u);
+        }
+        return r;
+    }
+    __device__ static inline void store(bf16_t* p, f32x8 v) {
+        __builtin_nontemporal_store(Tr<bf16_t>::narrow(v), (bf16x8*)p);
+    }
+};
+template <>
+struct Eight<float> {
+    typedef f32x8 raw;
+    __device__ static inline raw load(const float* p) {
+        return Tr<float>::ld8(p);
+    }
+    __device__ static inline f32x8 widen(raw v) { return v; }
+    __device__ static inline void store(float* p, f32x8 v) {
+        Tr<float>::st8(p, v);
+    }
+};
 
 __device__ inline float sigm(float v) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
 }
-
-// Sum over the lanes that share a row (WPR waves), the same in every lane.
-template <int WPR>
-__device__ inline float row_sum(float v, float* lds) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    if constexpr (WPR > 1) {
-        __syncthreads();  // the last sum's readers are done
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.f;
-#pragma unroll
-        for (int w = 0; w < WPR; ++w) v += lds[w];
-    }
-    return v;
-}
-
-template <int WPR>
-struct Place {
-    static constexpr int kLanes = 64 * WPR;
-    int lane;
-    __device__ Place() : lane(WPR == 1 ? threadIdx.x & 63 : threadIdx.x) {}
-    __device__ int col(int v) const { return (v * kLanes + lane) * kVec; }
-};
-
 __device__ inline float sum8(f32x8 v) {
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
-
-// silu(z) and its derivative.
 __device__ inline f32x8 silu8(f32x8 z) {
     f32x8 g;
 #pragma unroll
@@ -62,39 +77,83 @@ __device__ inline f32x8 silu8(f32x8 z) {
     return g;
 }
 
+// LANES < 64: a team is LANES lanes of a wave.  64: a wave, or (WIDE) all
+// waves of the workgroup.
+template <int LANES, bool WIDE, int V>
+struct Team {
+    int lane, stride;  // lane of the team; columns from one of the lane's vectors to the next
+    int64_t index, teams;
+    __device__ Team() {
+        const int per = WIDE ? 1 : (int)blockDim.x / LANES;
+        lane = WIDE ? (int)threadIdx.x : (int)threadIdx.x % LANES;
+        stride = (WIDE ? (int)blockDim.x : LANES) * kVec;
+        index = (int64_t)blockIdx.x * per + (WIDE ? 0 : (int)threadIdx.x / LANES);
+        teams = (int64_t)gridDim.x * per;
+    }
+    __device__ int col(int v) const { return v * stride + lane * kVec; }
+    // Sum over the team, the same in every lane.
+    __device__ float sum(float v, float* lds) const {
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) v += __shfl_xor(v, d);
+        if constexpr (WIDE) {
+            __syncthreads();  // the last sum's readers are done
+            if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+            __syncthreads();
+            v = 0.f;
+            for (int w = 0; w < (int)blockDim.x / 64; ++w) v += lds[w];
+        }
+        return v;
+    }
+};
+
 // ------------------------------------------------------------------ forward
 // KIND 0: residual norm (A: type of x and y, B: of the residual).
 // KIND 1: gated norm (A: type of z and y, B: of x); 2: the norm before the gate.
-template <typename A, typename B, int KIND, int WPR, int V>
-__global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(NormArgs a) {
-    __shared__ float lds[4];
-    const Place<WPR> p;
-    const int64_t seg = WPR == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-    if (seg >= a.rows * a.G) return;  // WPR 1: whole waves; else: whole workgroups
-    const int64_t row = seg / a.G;
-    const int n = a.D / a.G, g0 = (int)(seg - row * a.G) * n;
+template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
+__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void norm_forward_kernel(NormArgs a) {
+    __shared__ float lds[kMaxWaves];
+    const Team<LANES, WIDE, V> p;
+    const int64_t seg = p.index;
+    // WIDE: the whole workgroup has the row or not; else teams run apart, and a
+    // team without a row still takes part in its wave's shuffles
+    if (WIDE && seg >= a.rows * a.G) return;
+    const bool on = seg < a.rows * a.G;
+    const int64_t row = on ? seg / a.G : 0;
+    const int n = a.D / a.G, g0 = on ? (int)(seg - row * a.G) * n : 0;
     const A* xa = KIND == 0 ? (const A*)a.x + row * a.x_stride + g0 : (const A*)a.z + row * a.z_stride + g0;
     const B* xb = KIND == 0 ? (const B*)a.z + row * a.z_stride + g0 : (const B*)a.x + row * a.x_stride + g0;
+    typename Eight<A>::raw ra[V];
+    typename Eight<B>::raw rb[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = p.col(v);
+        ra[v] = {};
+        rb[v] = {};
+        if (on && c < n) {
+            ra[v] = Eight<A>::load(xa + c);
+            rb[v] = Eight<B>::load(xb + c);
+        }
+    }
     f32x8 u[V], gate[V];
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = p.col(v);
-        u[v] = f32x8{};
-        if (c < n) {
-            const f32x8 va = Tr<A>::widen(Tr<A>::ld8(xa + c));
-            const f32x8 vb = Tr<B>::widen(Tr<B>::ld8(xb + c));
-            if constexpr (KIND == 0) {
-                u[v] = a.scale ? vb + Tr<float>::ld8(a.scale + g0 + c) * va : vb + va;
-                Tr<B>::st8((B*)a.out + row * a.D + g0 + c, Tr<B>::narrow(u[v]));
-            } else {
-                gate[v] = silu8(va);
-                u[v] = KIND == 1 ? vb * gate[v] : vb;
+        const f32x8 va = Eight<A>::widen(ra[v]), vb = Eight<B>::widen(rb[v]);
+        if constexpr (KIND == 0) {
+            u[v] = vb + va;
+            if (on && c < n) {
+                if (a.scale) u[v] = vb + Tr<float>::ld8(a.scale + g0 + c) * va;
+                Eight<B>::store((B*)a.out + row * a.D + g0 + c, u[v]);
             }
-            ss += sum8(u[v] * u[v]);
+        } else {
+            gate[v] = silu8(va);
+            u[v] = KIND == 1 ? vb * gate[v] : vb;
         }
+        ss += sum8(u[v] * u[v]);
     }
-    const float rstd = 1.f / sqrtf(row_sum<WPR>(ss, lds) / (float)n + a.eps);
+    const float rstd = 1.f / sqrtf(p.sum(ss, lds) / (float)n + a.eps);
+    if (!on) return;
     if (a.rstd && p.lane == 0) a.rstd[seg] = rstd;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -102,7 +161,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(NormArgs a) 
         if (c < n) {
             f32x8 y = u[v] * rstd * Tr<float>::ld8(a.weight + g0 + c);
             if constexpr (KIND == 2) y *= gate[v];
-            Tr<A>::st8((A*)a.y + row * a.D + g0 + c, Tr<A>::narrow(y));
+            Eight<A>::store((A*)a.y + row * a.D + g0 + c, y);
         }
     }
 }
@@ -110,77 +169,108 @@ __global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(NormArgs a) 
 // ------------------------------------------------------------------ backward
 // With m = v rstd the normalised row and d the gradient of m w:
 //   dv = rstd (w d - m mean(w d m)),  dw = sum over rows of d m.
-// A workgroup takes every gridDim.x-th row (set of four rows) and keeps its
-// sums of dw (and dscale) in registers; they go to its own row of the partial
-// sums, which a second kernel adds in a fixed order.
-template <typename A, typename B, int KIND, int WPR, int V>
-__global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(NormArgs a) {
-    __shared__ float lds[4];
-    __shared__ f32x4 sums[WPR == 1 ? 3 * 64 * V * 2 : 1];
-    const Place<WPR> p;
+// Team k takes the rows k, k + teams, ..., the next one's data in flight, and
+// keeps its sums of dw (and dscale) in registers; a workgroup's go to its own row
+// of the partial sums, which a second kernel adds.
+template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
+__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void norm_backward_kernel(NormArgs a) {
+    __shared__ float lds[kMaxWaves];
+    __shared__ f32x4 sums[WIDE ? 1 : 3 * 64 * V * 2];
+    const Team<LANES, WIDE, V> p;
     const int n = a.D / a.G, g0 = blockIdx.y * n;
-    constexpr int kRows = WPR == 1 ? 4 : 1;
-    const int wave = WPR == 1 ? threadIdx.x >> 6 : 0;
     const bool scaled = KIND == 0 && a.dscale;
-    f32x8 w[V], dw[V] = {}, ds[V] = {};
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = p.col(v) < n ? Tr<float>::ld8(a.weight + g0 + p.col(v)) : f32x8{};
-    for (int64_t row = (int64_t)blockIdx.x * kRows + wave; row < a.rows; row += (int64_t)gridDim.x * kRows) {
-        const float rstd = a.rstd_in[row * a.G + blockIdx.y];
-        f32x8 m[V], wd[V], vx[V], vz[V];
-        float dot = 0.f;
+    // KIND 0: dy, the new residual, its gradient, x;  else: dy, x, z
+    struct Row {
+        typename Eight<A>::raw dy[V], za[V];
+        typename Eight<B>::raw xb[V], db[V];
+        float rstd;
+    };
+    auto load = [&](int64_t row, Row& r) {
+        const bool there = row < a.rows;
+        r.rstd = there ? a.rstd_in[row * a.G + blockIdx.y] : 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = p.col(v);
-            m[v] = wd[v] = vx[v] = vz[v] = f32x8{};
-            if (c < n) {
-                const f32x8 dy = Tr<A>::widen(Tr<A>::ld8((const A*)a.dy + row * a.D + g0 + c));
-                if constexpr (KIND == 0) {
-                    m[v] = Tr<B>::widen(Tr<B>::ld8((const B*)a.out + row * a.D + g0 + c)) * rstd;
-                    wd[v] = dy * w[v];
-                    dw[v] += dy * m[v];
-                } else {
-                    vx[v] = Tr<B>::widen(Tr<B>::ld8((const B*)a.x + row * a.x_stride + g0 + c));
-                    vz[v] = Tr<A>::widen(Tr<A>::ld8((const A*)a.z + row * a.z_stride + g0 + c));
-                    const f32x8 gate = silu8(vz[v]);
-                    m[v] = (KIND == 1 ? vx[v] * gate : vx[v]) * rstd;
-                    const f32x8 d = KIND == 1 ? dy : dy * gate;
-                    wd[v] = d * w[v];
-                    dw[v] += d * m[v];
-                    if constexpr (KIND == 2) vx[v] = dy;  // x itself is no longer needed
-                }
-                dot += sum8(wd[v] * m[v]);
+            r.dy[v] = r.za[v] = {};
+            r.xb[v] = r.db[v] = {};
+            if (!there || c >= n) continue;
+            const int64_t dense = row * a.D + g0 + c;
+            r.dy[v] = Eight<A>::load((const A*)a.dy + dense);
+            if constexpr (KIND == 0) {
+                r.xb[v] = Eight<B>::load((const B*)a.out + dense);
+                if (a.dout) r.db[v] = Eight<B>::load((const B*)a.dout + dense);
+                if (scaled) r.za[v] = Eight<A>::load((const A*)a.x + row * a.x_stride + g0 + c);
+            } else {
+                r.xb[v] = Eight<B>::load((const B*)a.x + row * a.x_stride + g0 + c);
+                r.za[v] = Eight<A>::load((const A*)a.z + row * a.z_stride + g0 + c);
             }
         }
-        const float mean = row_sum<WPR>(dot, lds) / (float)n;
+    };
+    f32x8 w[V], sc[V], dw[V] = {}, ds[V] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v] = p.col(v) < n ? Tr<float>::ld8(a.weight + g0 + p.col(v)) : f32x8{};
+        if (KIND == 0) sc[v] = a.scale && p.col(v) < n ? Tr<float>::ld8(a.scale + g0 + p.col(v)) : f32x8{1, 1, 1, 1, 1, 1, 1, 1};
+    }
+    constexpr bool kAhead = V < 4;  // there are no registers for the next row of the widest ones
+    Row cur, nxt;
+    if (kAhead) load(p.index, nxt);
+    // WIDE: the same rows for the whole workgroup; else as many rounds as the
+    // workgroup's first team has, so that a wave's teams stay together
+    const int64_t first = (int64_t)blockIdx.x * (WIDE ? 1 : (int)blockDim.x / LANES);
+    for (int64_t r0 = first, row = p.index; r0 < a.rows; r0 += p.teams, row += p.teams) {
+        if (kAhead) {
+            cur = nxt;
+            load(row + p.teams, nxt);
+        } else {
+            load(row, cur);
+        }
+        f32x8 m[V], wd[V];
+        float dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            f32x8 d = Eight<A>::widen(cur.dy[v]);
+            const f32x8 xb = Eight<B>::widen(cur.xb[v]);
+            if constexpr (KIND == 0) {
+                m[v] = xb * cur.rstd;
+            } else {
+                const f32x8 gate = silu8(Eight<A>::widen(cur.za[v]));
+                m[v] = (KIND == 1 ? xb * gate : xb) * cur.rstd;
+                if (KIND == 2) d *= gate;
+            }
+            wd[v] = d * w[v];
+            dw[v] += d * m[v];
+            dot += sum8(wd[v] * m[v]);
+        }
+        const float mean = p.sum(dot, lds) / (float)n;
+        if (row >= a.rows) continue;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = p.col(v);
             if (c >= n) continue;
-            f32x8 dv = (wd[v] - m[v] * mean) * rstd;
+            f32x8 dv = (wd[v] - m[v] * mean) * cur.rstd;
             if constexpr (KIND == 0) {
-                if (a.dout) dv += Tr<B>::widen(Tr<B>::ld8((const B*)a.dout + row * a.D + g0 + c));
-                if (a.dz) Tr<B>::st8((B*)a.dz + row * a.D + g0 + c, Tr<B>::narrow(dv));
-                if (scaled) ds[v] += dv * Tr<A>::widen(Tr<A>::ld8((const A*)a.x + row * a.x_stride + g0 + c));
-                if (a.dx) {
-                    if (a.scale) dv *= Tr<float>::ld8(a.scale + g0 + c);
-                    Tr<A>::st8((A*)a.dx + row * a.D + g0 + c, Tr<A>::narrow(dv));
-                }
+                dv += Eight<B>::widen(cur.db[v]);
+                const int64_t dense = row * a.D + g0 + c;
+                if (a.dz) Eight<B>::store((B*)a.dz + dense, dv);
+                if (scaled) ds[v] += dv * Eight<A>::widen(cur.za[v]);
+                Eight<A>::store((A*)a.dx + dense, dv * sc[v]);
             } else {
+                const f32x8 zv = Eight<A>::widen(cur.za[v]), xv = Eight<B>::widen(cur.xb[v]), dy = Eight<A>::widen(cur.dy[v]);
                 f32x8 dx, dz;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float z = vz[v][e], s = sigm(z), dsilu = s * (1.f + z * (1.f - s));
+                    const float z = zv[e], s = sigm(z), dsilu = s * (1.f + z * (1.f - s));
                     if (KIND == 1) {
                         dx[e] = dv[e] * (z * s);
-                        dz[e] = dv[e] * vx[v][e] * dsilu;
+                        dz[e] = dv[e] * xv[e] * dsilu;
                     } else {
                         dx[e] = dv[e];
-                        dz[e] = vx[v][e] * w[v][e] * m[v][e] * dsilu;
+                        dz[e] = dy[e] * w[v][e] * m[v][e] * dsilu;
                     }
                 }
-                Tr<B>::st8((B*)a.dx + row * a.dx_stride + g0 + c, Tr<B>::narrow(dx));
-                Tr<A>::st8((A*)a.dz + row * a.dz_stride + g0 + c, Tr<A>::narrow(dz));
+                Eight<B>::store((B*)a.dx + row * a.dx_stride + g0 + c, dx);
+                Eight<A>::store((A*)a.dz + row * a.dz_stride + g0 + c, dz);
             }
         }
     }
@@ -190,22 +280,30 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(NormArgs a)
         if (k == 1 && !scaled) break;
         f32x8(&s)[V] = k ? ds : dw;
         float* to = a.part + ((int64_t)k * a.nparts + blockIdx.x) * a.D + g0;
-        if constexpr (WPR == 1) {
+        if constexpr (!WIDE) {
+            // the wave's teams hold the same columns; then waves 1..3 through LDS
+#pragma unroll
+            for (int d = LANES; d < 64; d <<= 1)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[v][e] += __shfl_xor(s[v][e], d);
+            const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
             __syncthreads();
             if (wave) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    sums[(((wave - 1) * V + v) * 2) * 64 + p.lane] = __builtin_shufflevector(s[v], s[v], 0, 1, 2, 3);
-                    sums[(((wave - 1) * V + v) * 2 + 1) * 64 + p.lane] = __builtin_shufflevector(s[v], s[v], 4, 5, 6, 7);
+                    sums[(((wave - 1) * V + v) * 2) * 64 + lane] = __builtin_shufflevector(s[v], s[v], 0, 1, 2, 3);
+                    sums[(((wave - 1) * V + v) * 2 + 1) * 64 + lane] = __builtin_shufflevector(s[v], s[v], 4, 5, 6, 7);
                 }
             }
             __syncthreads();
-            if (wave) continue;
+            if (wave || lane >= LANES) continue;
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int o = 0; o < 3; ++o) {
-                    const f32x4 lo = sums[((o * V + v) * 2) * 64 + p.lane], hi = sums[((o * V + v) * 2 + 1) * 64 + p.lane];
+                    const f32x4 lo = sums[((o * V + v) * 2) * 64 + lane], hi = sums[((o * V + v) * 2 + 1) * 64 + lane];
                     s[v] += __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 }
         }
@@ -222,11 +320,15 @@ __global__ __launch_bounds__(kSumThreads) void column_sum_kernel(const float* pa
     if (threadIdx.x < kSumCols && col < cols) out[col] = s;
 }
 
-template <typename A, typename B, int KIND, int WPR, int V>
+// Threads of a workgroup for rows of n columns with LANES lanes a team.
+inline int norm_threads(int n, int V) { return (n + 64 * kVec * V - 1) / (64 * kVec * V) * 64; }
+
+template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
 hipError_t run_norm(const NormArgs& a, bool backward, hipStream_t stream) {
+    const int threads = WIDE ? norm_threads(a.D / a.G, V) : 256;
     if (backward) {
         if (a.rows > 0) {
-            hipLaunchKernelGGL((norm_backward_kernel<A, B, KIND, WPR, V>), dim3(a.nparts, a.G), dim3(kNormThreads), 0,
+            hipLaunchKernelGGL((norm_backward_kernel<A, B, KIND, LANES, WIDE, V>), dim3(a.nparts, a.G), dim3(threads), 0,
                                stream, a);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
@@ -235,32 +337,27 @@ hipError_t run_norm(const NormArgs& a, bool backward, hipStream_t stream) {
         if (e != hipSuccess || !a.dscale) return e;
         return launch_column_sum(a.part + (int64_t)a.nparts * a.D, a.rows > 0 ? a.nparts : 0, a.D, a.D, a.dscale, stream);
     }
-    const int64_t segs = a.rows * a.G, blocks = WPR == 1 ? (segs + 3) / 4 : segs;
+    const int64_t segs = a.rows * a.G, per = WIDE ? 1 : 256 / LANES;
     if (segs == 0) return hipSuccess;
-    hipLaunchKernelGGL((norm_forward_kernel<A, B, KIND, WPR, V>), dim3((unsigned)blocks), dim3(kNormThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_forward_kernel<A, B, KIND, LANES, WIDE, V>), dim3((unsigned)((segs + per - 1) / per)),
+                       dim3(threads), 0, stream, a);
     return hipGetLastError();
 }
+
+// Vectors of 8 columns a lane: as few as up to 8 waves a row allow.
+inline int norm_vectors(int n) { return n <= 4096 ? 1 : n <= 8192 ? 2 : 4; }
 
 template <typename A, typename B, int KIND>
 hipError_t by_columns(const NormArgs& a, bool backward, hipStream_t stream) {
     const int n = a.D / a.G;
-    if (n <= 4096) switch ((n + 511) / 512) {
-            case 1: return run_norm<A, B, KIND, 1, 1>(a, backward, stream);
-            case 2: return run_norm<A, B, KIND, 1, 2>(a, backward, stream);
-            case 3: return run_norm<A, B, KIND, 1, 3>(a, backward, stream);
-            case 4: return run_norm<A, B, KIND, 1, 4>(a, backward, stream);
-            case 5: return run_norm<A, B, KIND, 1, 5>(a, backward, stream);
-            case 6: return run_norm<A, B, KIND, 1, 6>(a, backward, stream);
-            default: return run_norm<A, B, KIND, 1, 8>(a, backward, stream);
-        }
-    switch ((n + 2047) / 2048) {
-        case 3: return run_norm<A, B, KIND, 4, 3>(a, backward, stream);
-        case 4: return run_norm<A, B, KIND, 4, 4>(a, backward, stream);
-        case 5:
-        case 6: return run_norm<A, B, KIND, 4, 6>(a, backward, stream);
-        case 7:
-        case 8: return run_norm<A, B, KIND, 4, 8>(a, backward, stream);
-        default: return hipErrorInvalidValue;
+    if (n <= 8 * kVec) return run_norm<A, B, KIND, 8, false, 1>(a, backward, stream);
+    if (n <= 16 * kVec) return run_norm<A, B, KIND, 16, false, 1>(a, backward, stream);
+    if (n <= 32 * kVec) return run_norm<A, B, KIND, 32, false, 1>(a, backward, stream);
+    if (n <= 64 * kVec) return run_norm<A, B, KIND, 64, false, 1>(a, backward, stream);
+    switch (norm_vectors(n)) {
+        case 1: return run_norm<A, B, KIND, 64, true, 1>(a, backward, stream);
+        case 2: return run_norm<A, B, KIND, 64, true, 2>(a, backward, stream);
+        default: return run_norm<A, B, KIND, 64, true, 4>(a, backward, stream);
     }
 }
 
@@ -275,9 +372,18 @@ hipError_t by_types(const NormArgs& a, bool backward, hipStream_t stream) {
 
 }  // namespace
 
+// Workgroups along the rows of the backward pass: what 256 compute units hold
+// at once over all groups (16 waves each, 8 with more than one vector a lane),
+// so that they run in one round; no more than there are rows for.
 int32_t norm_parts(int64_t rows, int32_t D, int32_t G) {
-    const int64_t per = D / G <= 4096 ? 4 : 1;  // rows a workgroup works on at once
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, std::max(1, 1024 / G)));
+    const int n = D / G, V = norm_vectors(n);
+    int per = 1, waves = norm_threads(n, V) / 64;  // rows at once and waves of a workgroup
+    if (n <= 64 * kVec) {
+        per = 256 / (n <= 8 * kVec ? 8 : n <= 16 * kVec ? 16 : n <= 32 * kVec ? 32 : 64);
+        waves = 4;
+    }
+    const int held = 256 * ((V == 1 ? 16 : 8) / waves);
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, std::max(1, held / G)));
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream) { return by_types<0>(a, false, stream); }
