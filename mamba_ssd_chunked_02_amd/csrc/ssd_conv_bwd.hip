@@ -215,31 +215,33 @@ __global__ __launch_bounds__(kBwdThreads) void conv_backward_kernel(ConvBwdArgs 
 // have pushed the row out.
 template <typename T, typename Y, int K, bool SILU>
 __global__ __launch_bounds__(kBwdThreads) void conv_backward_state_kernel(ConvBwdArgs a) {
-    const int64_t quads = a.C / kCh, id = (int64_t)blockIdx.x * kBwdThreads + threadIdx.x;
-    if (id >= a.nseq * quads) return;
-    const int64_t s = id / quads;
-    const int c0 = (int)(id - s * quads) * kCh;
-    const RowRange q = seq_range(a.cu, a.L, a.T, s);
-    const int64_t len = q.hi - q.lo;
-    const Taps4<K> tp = load_taps4<K>(a, c0);
-    const Part<Y> dyp = dy_part<Y>(a, c0);
-    f32x4 ds[K - 1] = {};
+    const int64_t quads = a.C / kCh;
+    for (int64_t id = (int64_t)blockIdx.x * kBwdThreads + threadIdx.x; id < a.nseq * quads;
+         id += (int64_t)gridDim.x * kBwdThreads) {
+        const int64_t s = id / quads;
+        const int c0 = (int)(id - s * quads) * kCh;
+        const RowRange q = seq_range(a.cu, a.L, a.T, s);
+        const int64_t len = q.hi - q.lo;
+        const Taps4<K> tp = load_taps4<K>(a, c0);
+        const Part<Y> dyp = dy_part<Y>(a, c0);
+        f32x4 ds[K - 1] = {};
 #pragma unroll
-    for (int t = 0; t < K - 1; ++t) {
-        if (t >= len) break;
-        f32x4 h[K];
+        for (int t = 0; t < K - 1; ++t) {
+            if (t >= len) break;
+            f32x4 h[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) h[k] = padded_input<T, K>(a, s, q, t + k, c0);
-        const f32x4 dv = dv_row<K, SILU>(tp, h, Tr<Y>::ld4(dyp.p + (q.lo + t) * dyp.stride));
+            for (int k = 0; k < K; ++k) h[k] = padded_input<T, K>(a, s, q, t + k, c0);
+            const f32x4 dv = dv_row<K, SILU>(tp, h, Tr<Y>::ld4(dyp.p + (q.lo + t) * dyp.stride));
 #pragma unroll
-        for (int k = 0; k + t < K - 1; ++k) ds[t + k] += tp.w[k] * dv;
-    }
+            for (int k = 0; k + t < K - 1; ++k) ds[t + k] += tp.w[k] * dv;
+        }
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-        // row j of the padded sequence is row j - len of the final state
-        if (a.dstate_out && j >= len)
-            ds[j] += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + j - len) * a.C + c0);
-        Tr<T>::st4((T*)a.dstate_in + (s * (K - 1) + j) * a.C + c0, ds[j]);
+        for (int j = 0; j < K - 1; ++j) {
+            // row j of the padded sequence is row j - len of the final state
+            if (a.dstate_out && j >= len)
+                ds[j] += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + j - len) * a.C + c0);
+            Tr<T>::st4((T*)a.dstate_in + (s * (K - 1) + j) * a.C + c0, ds[j]);
+        }
     }
 }
 
@@ -269,7 +271,8 @@ hipError_t run_conv_backward(const ConvBwdArgs& a, hipStream_t stream) {
     if (a.dstate_in && a.nseq > 0) {
         const int64_t n = a.nseq * (a.C / kCh);
         hipLaunchKernelGGL((conv_backward_state_kernel<T, Y, K, SILU>),
-                           dim3((unsigned)((n + kBwdThreads - 1) / kBwdThreads)), dim3(kBwdThreads), 0, stream, a);
+                           dim3((unsigned)std::min<int64_t>((n + kBwdThreads - 1) / kBwdThreads, 1 << 22)), dim3(kBwdThreads), 0,
+                           stream, a);
         return hipGetLastError();
     }
     return hipSuccess;

@@ -623,22 +623,23 @@ __global__ __launch_bounds__(kSumThreads) void gated_dlam_kernel(GatedArgs a, in
 template <typename T, typename Y>
 __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a, const float* state, float* state_out) {
     const int64_t quads = a.C / kLaneCh;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= a.nseq * quads) return;
-    const int64_t n = id / quads;
-    const int c0 = (int)(id - n * quads) * kLaneCh;
-    f32x4 h = *(const f32x4*)(state + n * a.C + c0), k = *(const f32x4*)(a.lam + c0);
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < a.nseq * quads; id += (int64_t)gridDim.x * 256) {
+        const int64_t n = id / quads;
+        const int c0 = (int)(id - n * quads) * kLaneCh;
+        f32x4 h = *(const f32x4*)(state + n * a.C + c0), k = *(const f32x4*)(a.lam + c0);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) k[c] = decay_factor(k[c], a.rate);
-    typedef typename Raw<T>::type raw;
-    const Step<T> st(k, false, *(const raw*)((const T*)a.x + n * a.x_stride + c0),
-                     *(const raw*)((const T*)a.r + n * a.r_stride + c0), *(const raw*)((const T*)a.i + n * a.i_stride + c0));
-    h = st.a * h + st.b;
-    *(f32x4*)(state_out + n * a.C + c0) = h;
-    Tr<Y>::st4((Y*)a.y + n * a.C + c0, h);
+        for (int c = 0; c < 4; ++c) k[c] = decay_factor(k[c], a.rate);
+        typedef typename Raw<T>::type raw;
+        const Step<T> st(k, false, *(const raw*)((const T*)a.x + n * a.x_stride + c0),
+                         *(const raw*)((const T*)a.r + n * a.r_stride + c0),
+                         *(const raw*)((const T*)a.i + n * a.i_stride + c0));
+        h = st.a * h + st.b;
+        *(f32x4*)(state_out + n * a.C + c0) = h;
+        Tr<Y>::st4((Y*)a.y + n * a.C + c0, h);
+    }
 }
 
-inline unsigned blocks_of(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+inline int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 // Clears what the pass publishes and plans a packed batch; nothing to do for
 // a dense batch of one tile.
@@ -684,7 +685,7 @@ hipError_t run_backward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream
                            dim3(kBwdTile / kBwdRows * kSegLanes), 0, stream, a, ps, part);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(gated_dlam_kernel, dim3(blocks_of(a.C, kSumCols)), dim3(kSumThreads), 0, stream, a, lay.ntiles,
+    hipLaunchKernelGGL(gated_dlam_kernel, dim3((unsigned)blocks_of(a.C, kSumCols)), dim3(kSumThreads), 0, stream, a, lay.ntiles,
                        (const float*)part, a.dlam);
     return hipGetLastError();
 }
@@ -693,7 +694,8 @@ template <typename T, typename Y>
 hipError_t run_gated_step(const GatedArgs& a, const float* state, float* state_out, hipStream_t stream) {
     const int64_t n = a.nseq * (a.C / kLaneCh);
     if (n == 0) return hipSuccess;
-    hipLaunchKernelGGL((gated_step_kernel<T, Y>), dim3(blocks_of(n, 256)), dim3(256), 0, stream, a, state, state_out);
+    hipLaunchKernelGGL((gated_step_kernel<T, Y>), dim3((unsigned)std::min<int64_t>(blocks_of(n, 256), 1 << 22)), dim3(256), 0, stream,
+                       a, state, state_out);
     return hipGetLastError();
 }
 

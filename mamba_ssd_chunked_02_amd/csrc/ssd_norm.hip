@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kVec = 8;
 constexpr int kMaxWaves = 8;
+constexpr int64_t kMaxBlocks = 1 << 22;  // a launch counts its lanes in 32 bits
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -113,55 +114,58 @@ template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
 __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void norm_forward_kernel(NormArgs a) {
     __shared__ float lds[kMaxWaves];
     const Team<LANES, WIDE, V> p;
-    const int64_t seg = p.index;
-    // WIDE: the whole workgroup has the row or not; else teams run apart, and a
-    // team without a row still takes part in its wave's shuffles
-    if (WIDE && seg >= a.rows * a.G) return;
-    const bool on = seg < a.rows * a.G;
-    const int64_t row = on ? seg / a.G : 0;
-    const int n = a.D / a.G, g0 = on ? (int)(seg - row * a.G) * n : 0;
-    const A* xa = KIND == 0 ? (const A*)a.x + row * a.x_stride + g0 : (const A*)a.z + row * a.z_stride + g0;
-    const B* xb = KIND == 0 ? (const B*)a.z + row * a.z_stride + g0 : (const B*)a.x + row * a.x_stride + g0;
-    typename Eight<A>::raw ra[V];
-    typename Eight<B>::raw rb[V];
+    const int n = a.D / a.G;
+    const int64_t segs = a.rows * a.G;
+    // as many rounds as the workgroup's first team has: a team without a row
+    // still takes part in its wave's shuffles
+    const int64_t first = (int64_t)blockIdx.x * (WIDE ? 1 : (int)blockDim.x / LANES);
+    for (int64_t s0 = first, seg = p.index; s0 < segs; s0 += p.teams, seg += p.teams) {
+        const bool on = seg < segs;
+        const int64_t row = on ? seg / a.G : 0;
+        const int g0 = on ? (int)(seg - row * a.G) * n : 0;
+        const A* xa = KIND == 0 ? (const A*)a.x + row * a.x_stride + g0 : (const A*)a.z + row * a.z_stride + g0;
+        const B* xb = KIND == 0 ? (const B*)a.z + row * a.z_stride + g0 : (const B*)a.x + row * a.x_stride + g0;
+        typename Eight<A>::raw ra[V];
+        typename Eight<B>::raw rb[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = p.col(v);
-        ra[v] = {};
-        rb[v] = {};
-        if (on && c < n) {
-            ra[v] = Eight<A>::load(xa + c);
-            rb[v] = Eight<B>::load(xb + c);
-        }
-    }
-    f32x8 u[V], gate[V];
-    float ss = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = p.col(v);
-        const f32x8 va = Eight<A>::widen(ra[v]), vb = Eight<B>::widen(rb[v]);
-        if constexpr (KIND == 0) {
-            u[v] = vb + va;
+        for (int v = 0; v < V; ++v) {
+            const int c = p.col(v);
+            ra[v] = {};
+            rb[v] = {};
             if (on && c < n) {
-                if (a.scale) u[v] = vb + Tr<float>::ld8(a.scale + g0 + c) * va;
-                Eight<B>::store((B*)a.out + row * a.D + g0 + c, u[v]);
+                ra[v] = Eight<A>::load(xa + c);
+                rb[v] = Eight<B>::load(xb + c);
             }
-        } else {
-            gate[v] = silu8(va);
-            u[v] = KIND == 1 ? vb * gate[v] : vb;
         }
-        ss += sum8(u[v] * u[v]);
-    }
-    const float rstd = 1.f / sqrtf(p.sum(ss, lds) / (float)n + a.eps);
-    if (!on) return;
-    if (a.rstd && p.lane == 0) a.rstd[seg] = rstd;
+        f32x8 u[V], gate[V];
+        float ss = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = p.col(v);
-        if (c < n) {
-            f32x8 y = u[v] * rstd * Tr<float>::ld8(a.weight + g0 + c);
-            if constexpr (KIND == 2) y *= gate[v];
-            Eight<A>::store((A*)a.y + row * a.D + g0 + c, y);
+        for (int v = 0; v < V; ++v) {
+            const int c = p.col(v);
+            const f32x8 va = Eight<A>::widen(ra[v]), vb = Eight<B>::widen(rb[v]);
+            if constexpr (KIND == 0) {
+                u[v] = vb + va;
+                if (on && c < n) {
+                    if (a.scale) u[v] = vb + Tr<float>::ld8(a.scale + g0 + c) * va;
+                    Eight<B>::store((B*)a.out + row * a.D + g0 + c, u[v]);
+                }
+            } else {
+                gate[v] = silu8(va);
+                u[v] = KIND == 1 ? vb * gate[v] : vb;
+            }
+            ss += sum8(u[v] * u[v]);
+        }
+        const float rstd = 1.f / sqrtf(p.sum(ss, lds) / (float)n + a.eps);
+        if (!on) continue;
+        if (a.rstd && p.lane == 0) a.rstd[seg] = rstd;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = p.col(v);
+            if (c < n) {
+                f32x8 y = u[v] * rstd * Tr<float>::ld8(a.weight + g0 + c);
+                if constexpr (KIND == 2) y *= gate[v];
+                Eight<A>::store((A*)a.y + row * a.D + g0 + c, y);
+            }
         }
     }
 }
@@ -339,8 +343,9 @@ hipError_t run_norm(const NormArgs& a, bool backward, hipStream_t stream) {
     }
     const int64_t segs = a.rows * a.G, per = WIDE ? 1 : 256 / LANES;
     if (segs == 0) return hipSuccess;
-    hipLaunchKernelGGL((norm_forward_kernel<A, B, KIND, LANES, WIDE, V>), dim3((unsigned)((segs + per - 1) / per)),
-                       dim3(threads), 0, stream, a);
+    const int64_t blocks = std::min<int64_t>((segs + per - 1) / per, kMaxBlocks);
+    hipLaunchKernelGGL((norm_forward_kernel<A, B, KIND, LANES, WIDE, V>), dim3((unsigned)blocks), dim3(threads), 0, stream,
+                       a);
     return hipGetLastError();
 }
 
