@@ -15,6 +15,7 @@ and what it returned.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Sequence
 
@@ -98,6 +99,26 @@ def _query(name, *args) -> int:
     return need.value
 
 
+# Workspace bytes: a function of the sizes alone, asked for once for each.
+@functools.lru_cache(maxsize=1024)
+def _gated_bytes(batch, seqlen, channels, packed, backward) -> int:
+    sh = _GatedShape(batch, seqlen, channels, SSD_F32, SSD_F32, 1.0)
+    sh.cu_seqlens = 16 if packed else None  # only whether there are offsets counts
+    return _query("ssd_gated_scan_workspace_size", ctypes.byref(sh), backward)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bytes(rows, columns, groups) -> int:
+    return _query("ssd_norm_backward_workspace_size", ctypes.byref(_NormShape(rows, columns, groups)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_bytes(batch, seqlen, channels, width, packed) -> int:
+    sh = _ConvShape(batch, seqlen, channels, width)
+    sh.cu_seqlens = 16 if packed else None
+    return _query("ssd_causal_conv1d_backward_workspace_size", ctypes.byref(sh))
+
+
 def _gpu(first, *others) -> int:
     """All tensors on one GPU; returns its index."""
     index = first.get_device()
@@ -159,6 +180,9 @@ def _p(t):
 
 
 def _new(like, shape, dtype):
+    """A new dense tensor on `like`'s device."""
+    if like.dtype == dtype and like.shape == shape and like.is_contiguous():
+        return _torch().empty_like(like)
     return like.new_empty(shape, dtype=dtype)
 
 
@@ -243,7 +267,7 @@ def gated_scan(x, r, i, lam, *, rate: float = 8.0, init_state=None, cu_seqlens=N
         final_state = _new(x, state, f32)
     states = _new(x, _states_shape(x), f32) if want_states else None
     ref = ctypes.byref(sh)
-    workspace = _workspace(workspace, _query("ssd_gated_scan_workspace_size", ref, 0), x)
+    workspace = _workspace(workspace, _gated_bytes(sh.batch, sh.seqlen, sh.channels, cu_seqlens is not None, 0), x)
     _launch(index, "ssd_gated_scan", x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _p(init_state),
             y.data_ptr(), _p(final_state), _p(states), ref, workspace.data_ptr(), _bytes(workspace))
     del keep
@@ -288,7 +312,7 @@ def gated_scan_backward(dy, x, r, i, lam, states, *, rate: float = 8.0, init_sta
     if dinit_state is None and want_dinit:
         dinit_state = _new(x, state, f32)
     ref = ctypes.byref(sh)
-    workspace = _workspace(workspace, _query("ssd_gated_scan_workspace_size", ref, 1), x)
+    workspace = _workspace(workspace, _gated_bytes(sh.batch, sh.seqlen, sh.channels, cu_seqlens is not None, 1), x)
     _launch(index, "ssd_gated_scan_backward", dy.data_ptr(), _p(dfinal_state), x.data_ptr(), r.data_ptr(),
             i.data_ptr(), lam.data_ptr(), _p(init_state), states.data_ptr(), *[t.data_ptr() for t in grads],
             dlam.data_ptr(), _p(dinit_state), ref, workspace.data_ptr(), _bytes(workspace))
@@ -385,7 +409,7 @@ def add_rms_norm_backward(dy, residual_out, weight, rstd, *, dresidual_out=None,
     dweight = _new(weight, weight.shape, f32)
     dscale = None if scale is None else _new(scale, scale.shape, f32)
     ref = ctypes.byref(sh)
-    workspace = _workspace(workspace, _query("ssd_norm_backward_workspace_size", ref), dy)
+    workspace = _workspace(workspace, _norm_bytes(sh.rows, sh.columns, sh.groups), dy)
     _launch(index, "ssd_add_rms_norm_backward", dy.data_ptr(), _p(dresidual_out), residual_out.data_ptr(),
             weight.data_ptr(), rstd.data_ptr(), None if scale is None else x.data_ptr(), _p(scale), dx.data_ptr(),
             None if one else dresidual.data_ptr(), dweight.data_ptr(), _p(dscale), ref, workspace.data_ptr(),
@@ -438,7 +462,7 @@ def gated_rms_norm_backward(dy, x, z, weight, rstd, *, groups: int = 1, norm_bef
     sh.dx_stride, sh.dz_stride = _row_stride(dx, "dx"), _row_stride(dz, "dz")
     dweight = _new(weight, weight.shape, f32)
     ref = ctypes.byref(sh)
-    workspace = _workspace(workspace, _query("ssd_norm_backward_workspace_size", ref), x)
+    workspace = _workspace(workspace, _norm_bytes(sh.rows, sh.columns, sh.groups), x)
     _launch(index, "ssd_gated_rms_norm_backward", dy.data_ptr(), x.data_ptr(), z.data_ptr(), weight.data_ptr(),
             rstd.data_ptr(), dx.data_ptr(), dz.data_ptr(), dweight.data_ptr(), ref, workspace.data_ptr(),
             _bytes(workspace))
@@ -481,7 +505,7 @@ def causal_conv1d_backward(dys, x, weight, bias=None, *, cu_seqlens=None, cu_seq
     want = conv_state is not None if want_dstate is None else want_dstate
     dstate = _new(x, state, x.dtype) if want else None
     ref = ctypes.byref(sh)
-    workspace = _workspace(workspace, _query("ssd_causal_conv1d_backward_workspace_size", ref), x)
+    workspace = _workspace(workspace, _conv_bytes(sh.batch, sh.seqlen, C, K, cu_seqlens is not None), x)
     _launch(index, "ssd_causal_conv1d_backward", ctypes.byref(parts), x.data_ptr(), weight.data_ptr(), _p(bias),
             _p(conv_state), _p(dfinal_conv_state), dx.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dstate), ref,
             workspace.data_ptr(), _bytes(workspace))

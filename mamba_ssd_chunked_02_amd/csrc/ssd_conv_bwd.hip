@@ -84,12 +84,51 @@ __device__ inline f32x4 padded_input(const ConvBwdArgs& a, int64_t s, RowRange q
     return Tr<T>::ld4((const T*)a.x + (q.lo + j - (K - 1)) * a.C + c0);
 }
 
+// Gradient of the incoming state of sequence s: row j of it is an input of the
+// tokens t < j + 1,
+//   dstate[j] = sum over k <= j, j - k < length of w[k] dv[j - k],
+// plus the final state's own gradient where the sequence is too short to
+// have pushed the row out.
+template <typename T, typename Y, int K, bool SILU>
+__device__ inline void state_gradient(const ConvBwdArgs& a, int64_t s, int c0) {
+    const RowRange q = seq_range(a.cu, a.L, a.T, s);
+    const int64_t len = q.hi - q.lo;
+    const Taps4<K> tp = load_taps4<K>(a, c0);
+    const Part<Y> dyp = dy_part<Y>(a, c0);
+    f32x4 ds[K - 1] = {};
+#pragma unroll
+    for (int t = 0; t < K - 1; ++t) {
+        if (t >= len) break;
+        f32x4 h[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) h[k] = padded_input<T, K>(a, s, q, t + k, c0);
+        const f32x4 dv = dv_row<K, SILU>(tp, h, Tr<Y>::ld4(dyp.p + (q.lo + t) * dyp.stride));
+#pragma unroll
+        for (int k = 0; k + t < K - 1; ++k) ds[t + k] += tp.w[k] * dv;
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        // row j of the padded sequence is row j - len of the final state
+        if (a.dstate_out && j >= len)
+            ds[j] += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + j - len) * a.C + c0);
+        Tr<T>::st4((T*)a.dstate_in + (s * (K - 1) + j) * a.C + c0, ds[j]);
+    }
+}
+
+// Workgroups blockIdx.x < a.nblocks: a block of rows; the others: the incoming
+// states' gradients, a sequence a wave.
 template <typename T, typename Y, int K, bool SILU>
 __global__ __launch_bounds__(kBwdThreads) void conv_backward_kernel(ConvBwdArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int c = blockIdx.y * kWaveCh + lane * kCh;
     const bool on = c < a.C;
     const int c0 = on ? c : a.C - kCh;
+    if ((int)blockIdx.x >= a.nblocks) {
+        const int64_t stride = ((int64_t)gridDim.x - a.nblocks) * 4;
+        for (int64_t s = ((int64_t)blockIdx.x - a.nblocks) * 4 + wave; on && s < a.nseq; s += stride)
+            state_gradient<T, Y, K, SILU>(a, s, c0);
+        return;
+    }
     const int rows = a.block_rows / 4;  // rows of a wave
     const int64_t r0 = min((int64_t)blockIdx.x * a.block_rows + wave * rows, a.T), r1 = min(r0 + rows, a.T);
     const RowRange live = live_rows(a.cu, a.nseq, a.T);
@@ -209,42 +248,6 @@ __global__ __launch_bounds__(kBwdThreads) void conv_backward_kernel(ConvBwdArgs 
     }
 }
 
-// Gradient of the incoming state: row j of it is an input of the tokens t < j + 1,
-//   dstate[j] = sum over k <= j, j - k < length of w[k] dv[j - k],
-// plus the final state's own gradient where the sequence is too short to
-// have pushed the row out.
-template <typename T, typename Y, int K, bool SILU>
-__global__ __launch_bounds__(kBwdThreads) void conv_backward_state_kernel(ConvBwdArgs a) {
-    const int64_t quads = a.C / kCh;
-    for (int64_t id = (int64_t)blockIdx.x * kBwdThreads + threadIdx.x; id < a.nseq * quads;
-         id += (int64_t)gridDim.x * kBwdThreads) {
-        const int64_t s = id / quads;
-        const int c0 = (int)(id - s * quads) * kCh;
-        const RowRange q = seq_range(a.cu, a.L, a.T, s);
-        const int64_t len = q.hi - q.lo;
-        const Taps4<K> tp = load_taps4<K>(a, c0);
-        const Part<Y> dyp = dy_part<Y>(a, c0);
-        f32x4 ds[K - 1] = {};
-#pragma unroll
-        for (int t = 0; t < K - 1; ++t) {
-            if (t >= len) break;
-            f32x4 h[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) h[k] = padded_input<T, K>(a, s, q, t + k, c0);
-            const f32x4 dv = dv_row<K, SILU>(tp, h, Tr<Y>::ld4(dyp.p + (q.lo + t) * dyp.stride));
-#pragma unroll
-            for (int k = 0; k + t < K - 1; ++k) ds[t + k] += tp.w[k] * dv;
-        }
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-            // row j of the padded sequence is row j - len of the final state
-            if (a.dstate_out && j >= len)
-                ds[j] += Tr<T>::ld4((const T*)a.dstate_out + (s * (K - 1) + j - len) * a.C + c0);
-            Tr<T>::st4((T*)a.dstate_in + (s * (K - 1) + j) * a.C + c0, ds[j]);
-        }
-    }
-}
-
 // dweight [C, K] and dbias [C] from the workgroups' sums.
 template <int K>
 __global__ __launch_bounds__(kSumThreads) void conv_backward_sum_kernel(ConvBwdArgs a, int64_t n) {
@@ -256,26 +259,19 @@ __global__ __launch_bounds__(kSumThreads) void conv_backward_sum_kernel(ConvBwdA
 }
 
 template <typename T, typename Y, int K, bool SILU>
-hipError_t run_conv_backward(const ConvBwdArgs& a, hipStream_t stream) {
-    hipError_t e;
-    if (a.T > 0) {
+hipError_t run_conv_backward(ConvBwdArgs a, hipStream_t stream) {
+    const int64_t states = a.dstate_in ? std::min<int64_t>((a.nseq + 3) / 4, 1 << 20) : 0;
+    a.nblocks = a.T > 0 ? a.nblocks : 0;
+    if (a.nblocks + states > 0) {
         hipLaunchKernelGGL((conv_backward_kernel<T, Y, K, SILU>),
-                           dim3((unsigned)a.nblocks, (unsigned)((a.C + kWaveCh - 1) / kWaveCh)), dim3(kBwdThreads), 0,
-                           stream, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+                           dim3((unsigned)(a.nblocks + states), (unsigned)((a.C + kWaveCh - 1) / kWaveCh)),
+                           dim3(kBwdThreads), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((conv_backward_sum_kernel<K>), dim3((unsigned)((a.C + kSumCols - 1) / kSumCols), K + 1),
-                       dim3(kSumThreads), 0, stream, a,
-                       (int64_t)(a.T > 0 ? a.nblocks : 0));
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (a.dstate_in && a.nseq > 0) {
-        const int64_t n = a.nseq * (a.C / kCh);
-        hipLaunchKernelGGL((conv_backward_state_kernel<T, Y, K, SILU>),
-                           dim3((unsigned)std::min<int64_t>((n + kBwdThreads - 1) / kBwdThreads, 1 << 22)), dim3(kBwdThreads), 0,
-                           stream, a);
-        return hipGetLastError();
-    }
-    return hipSuccess;
+                       dim3(kSumThreads), 0, stream, a, (int64_t)a.nblocks);
+    return hipGetLastError();
 }
 
 template <typename T, typename Y>

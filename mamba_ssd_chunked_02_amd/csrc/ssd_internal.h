@@ -314,9 +314,6 @@ struct ConvBwdArgs {
 void conv_backward_blocks(int64_t T, int32_t C, int32_t* nblocks, int32_t* block_rows);
 hipError_t launch_conv1d_backward(const ConvBwdArgs& a, hipStream_t stream);
 
-// out[c] = sum over n of part[n * ld + c], in a fixed order (ssd_norm.hip).
-hipError_t launch_column_sum(const float* part, int64_t n, int64_t ld, int32_t cols, float* out, hipStream_t stream);
-
 // Sets the sentence ssd_last_error_detail() returns on this thread (for
 // entry points outside ssd_api.cpp); returns st.
 int32_t set_error_detail(int32_t st, const char* fmt, ...);

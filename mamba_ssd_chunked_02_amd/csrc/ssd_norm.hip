@@ -317,11 +317,12 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void n
     }
 }
 
-__global__ __launch_bounds__(kSumThreads) void column_sum_kernel(const float* part, int64_t n, int64_t ld, int cols,
-                                                                 float* out) {
+// dweight (blockIdx.y 0) and dscale (1) from the workgroups' partial sums.
+__global__ __launch_bounds__(kSumThreads) void norm_sums_kernel(NormArgs a, int64_t n) {
     const int col = blockIdx.x * kSumCols + threadIdx.x % kSumCols;
-    const float s = column_sum(n, [&](int64_t t) { return col < cols ? part[t * ld + col] : 0.f; });
-    if (threadIdx.x < kSumCols && col < cols) out[col] = s;
+    const float* part = a.part + (int64_t)blockIdx.y * a.nparts * a.D;
+    const float s = column_sum(n, [&](int64_t t) { return col < a.D ? part[t * a.D + col] : 0.f; });
+    if (threadIdx.x < kSumCols && col < a.D) (blockIdx.y ? a.dscale : a.dweight)[col] = s;
 }
 
 // Threads of a workgroup for rows of n columns with LANES lanes a team.
@@ -337,9 +338,9 @@ hipError_t run_norm(const NormArgs& a, bool backward, hipStream_t stream) {
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
-        const hipError_t e = launch_column_sum(a.part, a.rows > 0 ? a.nparts : 0, a.D, a.D, a.dweight, stream);
-        if (e != hipSuccess || !a.dscale) return e;
-        return launch_column_sum(a.part + (int64_t)a.nparts * a.D, a.rows > 0 ? a.nparts : 0, a.D, a.D, a.dscale, stream);
+        hipLaunchKernelGGL(norm_sums_kernel, dim3((a.D + kSumCols - 1) / kSumCols, a.dscale ? 2 : 1), dim3(kSumThreads), 0,
+                           stream, a, (int64_t)(a.rows > 0 ? a.nparts : 0));
+        return hipGetLastError();
     }
     const int64_t segs = a.rows * a.G, per = WIDE ? 1 : 256 / LANES;
     if (segs == 0) return hipSuccess;
@@ -398,11 +399,6 @@ hipError_t launch_gated_norm(const NormArgs& a, hipStream_t stream) {
 }
 hipError_t launch_gated_norm_backward(const NormArgs& a, hipStream_t stream) {
     return a.norm_first ? by_types<2>(a, true, stream) : by_types<1>(a, true, stream);
-}
-
-hipError_t launch_column_sum(const float* part, int64_t n, int64_t ld, int32_t cols, float* out, hipStream_t stream) {
-    hipLaunchKernelGGL(column_sum_kernel, dim3((cols + kSumCols - 1) / kSumCols), dim3(kSumThreads), 0, stream, part, n, ld, cols, out);
-    return hipGetLastError();
 }
 
 }  // namespace ssd
