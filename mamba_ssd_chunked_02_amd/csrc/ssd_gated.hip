@@ -337,7 +337,7 @@ template <int WAVES>
 __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, int C, float Pt, float Ht, f32x2* group_s) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool on = chan < C;
-    const int at = on ? chan : 0;
+    const int at = on ? chan : 0;  // a lane without a channel reads there and waits for nothing
     const int p = (int)(ord % kGroup);
     const int64_t g = ord / kGroup;
     // wave 0 asks for the group's entry along with the maps
@@ -353,7 +353,7 @@ __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, i
 #pragma unroll
             for (int j = 0; j < kEach; ++j) {
                 v[j] = j0 + j < p ? look(m + (int64_t)j * C) : 0;
-                ready &= there(v[j]);
+                ready &= !on || there(v[j]);
             }
             if (__all(ready)) break;
             __builtin_amdgcn_s_sleep(1);
@@ -370,8 +370,8 @@ __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, i
         Pp = chain(Pp, m[0]);
     }
     // a sequence that starts in the group needs nothing from before it
-    if (g > 0 && !__all(is_reset(Pp))) {
-        while (!__all(there(e))) {
+    if (g > 0 && !__all(!on || is_reset(Pp))) {
+        while (!__all(!on || there(e))) {
             __builtin_amdgcn_s_sleep(1);
             e = look(ps.entry + g * C + at);
         }
