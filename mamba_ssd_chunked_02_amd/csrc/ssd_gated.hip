@@ -281,8 +281,19 @@ __device__ inline f32x4 run_factor(f32x4 S, bool reset) {
     return P;
 }
 
+// The workgroup's channel block.  Workgroups go to the 8 XCDs in turn; by_rows
+// gives consecutive workgroups of one XCD consecutive channel blocks, so that
+// an XCD reads and writes whole rows instead of every eighth 128 bytes of them
+// (49152 rows of 8192 channels 631 us, channel blocks in launch order 691 us;
+// forward and backward over 65536 rows of 2560 channels 842 against 920 us).  A
+// pass of a single round of workgroups is quicker in launch order (4096 rows of
+// 1536 channels 18.7 against 19.8 us).
+__device__ inline int channel_block(const GatedPass& ps) {
+    return (ps.by_rows ? blockIdx.x / 8 : blockIdx.x) % ps.nblocks;
+}
+
 // Which tile this workgroup has: the channel block's next one, in the pass's
-// order.
+// order (behind the last tile, where there are more workgroups than tiles: none).
 __device__ inline int64_t next_tile(const GatedPass& ps, int cb, uint32_t* slot) {
     if (!ps.counters) return 0;
     if (threadIdx.x == 0) *slot = atomicAdd(ps.counters + cb * kGatedCounterStride, 1u);
@@ -390,10 +401,11 @@ __global__ __launch_bounds__(kFwdTile / kFwdRows * kSegLanes) void gated_forward
     __shared__ f32x4 P_s[kRuns][kSegLanes], H_s[kRuns][kSegLanes];
     __shared__ f32x2 group_s[kGroup * kTileCh];
     const int seg = threadIdx.x / kSegLanes, ln = threadIdx.x % kSegLanes;
-    const int cb = blockIdx.x % ps.nblocks;
+    const int cb = channel_block(ps);
     if (threadIdx.x < kTileCh)
         k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
     const int64_t tile = next_tile(ps, cb, &slot);
+    if (tile >= ps.ntiles) return;  // the whole workgroup
     const Run<R, kFwdTile> u(a, tile, cb);
     typename Raw<T>::type xv[R], rv[R], iv[R];
     load_rows<T>(a, u, a.r, a.r_stride, rv);
@@ -473,10 +485,11 @@ __global__ __launch_bounds__(kBwdTile / kBwdRows * kSegLanes, sizeof(T) == 2 ? 4
     __shared__ f32x4 P_s[kRuns][kSegLanes], H_s[kRuns][kSegLanes], R_s[kRuns][kSegLanes], Q_s[kRuns][kSegLanes];
     __shared__ f32x2 group_s[kGroup * kTileCh];
     const int seg = threadIdx.x / kSegLanes, ln = threadIdx.x % kSegLanes;
-    const int cb = blockIdx.x % ps.nblocks;
+    const int cb = channel_block(ps);
     if (threadIdx.x < kTileCh)
         k_s[threadIdx.x] = decay_factor(a.lam[min(cb * kTileCh + (int)threadIdx.x, a.C - 1)], a.rate);
     const int64_t ord = next_tile(ps, cb, &slot), tile = ps.ntiles - 1 - ord;
+    if (tile < 0) return;  // the whole workgroup
     const Run<R, kBwdTile> u(a, tile, cb);
     typename Raw<T>::type xv[R], rv[R], iv[R];
     typename Raw<Y>::type dv[R];
@@ -581,11 +594,11 @@ __global__ __launch_bounds__(kBwdTile / kBwdRows * kSegLanes, sizeof(T) == 2 ? 4
             // 1 - a^2 = 0 only where log a is 0, and its square root's reciprocal meets that factor below;
             // a floor (the least normal number) keeps their product 0 (a NaN passes)
             const float m = d.m[c] < 0x1p-126f ? 0x1p-126f : d.m[c];
-            const float rb = __builtin_amdgcn_rsqf(m), beta = d.m[c] * rb;
-            const float dl0 = q[c] * (b[j][c] - d.a[c] * rb * si[j][c] * x[c]) * (k[c] * sr[j][c]);
-            dx[c] = g[c] * beta * si[j][c];
-            di[c] = dx[c] * x[c] * (1.f - si[j][c]);
-            dr[c] = dl0 * (1.f - sr[j][c]);
+            const float u = __builtin_amdgcn_rsqf(m) * si[j][c];  // sig(i) / beta
+            const float dl0 = q[c] * __builtin_fmaf(-d.a[c] * u, x[c], b[j][c]) * sr[j][c];  // dloga loga / k
+            dx[c] = g[c] * (d.m[c] * u);
+            di[c] = dx[c] * __builtin_fmaf(-x[c], si[j][c], x[c]);
+            dr[c] = dl0 * __builtin_fmaf(-k[c], sr[j][c], k[c]);
             dl[c] += dl0;
         }
         pin(q);
@@ -598,7 +611,7 @@ __global__ __launch_bounds__(kBwdTile / kBwdRows * kSegLanes, sizeof(T) == 2 ? 4
         }
     }
     __syncthreads();
-    P_s[seg][ln] = dl;
+    P_s[seg][ln] = dl * k;
     __syncthreads();
     if (threadIdx.x < kTileCh) {
         float s = 0.f;
@@ -641,12 +654,18 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a, const floa
 
 inline int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
+// Workgroups of a pass; by rows, the XCDs take equal numbers of tiles.
+inline int64_t pass_blocks(const GatedPass& ps) {
+    return (ps.by_rows ? (ps.ntiles + 7) / 8 * 8 : ps.ntiles) * ps.nblocks;
+}
+
 // Clears what the pass publishes and plans a packed batch; nothing to do for
 // a dense batch of one tile.
 hipError_t run_plan(GatedArgs& a, const GatedLayout& lay, char* ws, const float* in, float* out, GatedPass* ps,
                     hipStream_t stream) {
     const bool many = lay.ntiles > 1;
-    *ps = GatedPass{lay.ntiles, (int32_t)blocks_of(a.C, kTileCh), nullptr, nullptr, nullptr};
+    *ps = GatedPass{lay.ntiles, (int32_t)blocks_of(a.C, kTileCh), 0, nullptr, nullptr, nullptr};
+    ps->by_rows = lay.ntiles * ps->nblocks > 1024;  // more than a round of 4 workgroups a compute unit
     GatedPlan pl{nullptr, 0, nullptr, 0, nullptr, in, nullptr};
     if (many) {
         pl.words = ps->maps = (uint64_t*)(ws + lay.maps);
@@ -669,7 +688,7 @@ hipError_t run_forward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream_
     GatedPass ps;
     const hipError_t e = run_plan(a, lay, ws, a.init, a.final_state, &ps, stream);
     if (e != hipSuccess || a.T == 0) return e;
-    hipLaunchKernelGGL((gated_forward_kernel<T, Y>), dim3((unsigned)(lay.ntiles * ps.nblocks)),
+    hipLaunchKernelGGL((gated_forward_kernel<T, Y>), dim3((unsigned)pass_blocks(ps)),
                        dim3(kFwdTile / kFwdRows * kSegLanes), 0, stream, a, ps);
     return hipGetLastError();
 }
@@ -681,7 +700,7 @@ hipError_t run_backward(GatedArgs a, const GatedLayout& lay, char* ws, hipStream
     if (e != hipSuccess) return e;
     float* part = (float*)(ws + lay.dlam);
     if (a.T > 0) {
-        hipLaunchKernelGGL((gated_backward_kernel<T, Y>), dim3((unsigned)(lay.ntiles * ps.nblocks)),
+        hipLaunchKernelGGL((gated_backward_kernel<T, Y>), dim3((unsigned)pass_blocks(ps)),
                            dim3(kBwdTile / kBwdRows * kSegLanes), 0, stream, a, ps, part);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }

@@ -232,6 +232,7 @@ constexpr int kGatedCounterStride = 32;
 struct GatedPass {
     int64_t ntiles;
     int32_t nblocks;     // channel blocks
+    int32_t by_rows;     // consecutive workgroups of an XCD take consecutive channel blocks
     uint64_t* maps;
     uint64_t* entry;
     uint32_t* counters;  // NULL: one tile, nothing to share
