@@ -53,6 +53,7 @@ def _lib():
         vp, sz = ctypes.c_void_p, ctypes.c_size_t
         szp = ctypes.POINTER(sz)
         gsp, nsp, csp = (ctypes.POINTER(t) for t in (_GatedShape, _NormShape, _ConvShape))
+        declared = {}
         for name, args in {
                 "ssd_gated_scan_workspace_size": [gsp, ctypes.c_int32, szp],
                 "ssd_gated_scan": [vp] * 8 + [gsp, vp, sz, vp],
@@ -68,9 +69,10 @@ def _lib():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_int32
-            _functions[name] = f
+            declared[name] = f
         torch = _torch()
         _codes.update({torch.float32: SSD_F32, torch.bfloat16: SSD_BF16})
+        _functions.update(declared)  # all at once: another thread sees none or every one
     return lib
 
 

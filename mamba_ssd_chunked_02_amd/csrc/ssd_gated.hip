@@ -668,7 +668,7 @@ hipError_t run_plan(GatedArgs& a, const GatedLayout& lay, char* ws, const float*
                     hipStream_t stream) {
     const bool many = lay.ntiles > 1;
     *ps = GatedPass{lay.ntiles, (int32_t)blocks_of(a.C, kTileCh), 0, nullptr, nullptr, nullptr};
-    ps->by_rows = lay.ntiles * ps->nblocks > 1024;  // more than a round of 4 workgroups a compute unit
+    ps->by_rows = many && lay.ntiles * ps->nblocks > 1024;  // more than a round of 4 workgroups a compute unit
     GatedPlan pl{nullptr, 0, nullptr, 0, nullptr, in, nullptr};
     if (many) {
         pl.words = ps->maps = (uint64_t*)(ws + lay.maps);

@@ -266,6 +266,62 @@ def test_other_stream_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(out, want)), "replay %d" % k
 
 
+def test_two_calls_at_once():
+    """Passes of many tiles on two streams side by side, over and over, each the bits it gives alone."""
+    say("case: gated two streams")
+    C, args = 520, []
+    for k in range(2):
+        d = make(31 + k, [64] * 4, C, "bf16")
+        x, r, i = (up(np.tile(d[n], (16 + 8 * k, 1)), "bf16").view(2, -1, C) for n in ("x", "r", "i"))
+        args.append((x, r, i, up(d["lam"])))
+
+    def both(a):
+        y, fin, st = ssd.gated_scan(*a, want_states=True)
+        return (y, fin, *ssd.gated_scan_backward(y, *a, st, dfinal_state=fin))
+    want = [both(a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [[], []]
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(both(args[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(a, b) for run in got[k] for a, b in zip(run, want[k]))
+
+
+def test_one_tile_of_very_many_channels():
+    say("case: gated many channels")
+    C, L = 66056, 5
+    d = make(41, [L], C, "f32")
+    cols = np.r_[0:64, 32000:32064, C - 72:C]
+    args = [up(d[k]).view(1, L, C) for k in ("x", "r", "i")] + [up(d["lam"])]
+    y, fin, st = ssd.gated_scan(*args, init_state=up(d["init"]), want_states=True)
+    got = ssd.gated_scan_backward(up(d["dy"]).view(1, L, C), *args, st, init_state=up(d["init"]),
+                                  dfinal_state=up(d["dfinal"]))
+    part = {k: v[..., cols] for k, v in d.items()}
+    yr, fr, scale = block.gated_scan(part["x"], part["r"], part["i"], part["lam"], [L], 8.0, part["init"])
+    within(y[0][:, cols], yr, scale, 80, "f32", "y")
+    ref, sc = block.gated_scan_backward(part["dy"], part["x"], part["r"], part["i"], part["lam"], [L], 8.0, part["init"],
+                                        part["dfinal"])
+    for k, v in zip(("dx", "dr", "di", "dlam", "dinit"), got):
+        within(v.reshape(-1, C)[:, cols].reshape(ref[k].shape), ref[k], sc[k], 2 * 80 + 128, "f32", k)
+
+
+def test_no_sequences_and_no_tokens():
+    say("case: gated empty")
+    lam = torch.zeros(16, device="cuda")
+    for b, L in ((0, 7), (3, 0)):
+        x = torch.zeros(b, L, 16, device="cuda")
+        h = torch.randn(b, 16, device="cuda")
+        y, fin, st = ssd.gated_scan(x, x, x, lam, init_state=h, want_states=True)
+        assert y.shape == x.shape and torch.equal(fin, h) and st.shape == (0, 16)
+        dx, _, _, dlam, dinit = ssd.gated_scan_backward(x, x, x, x, lam, st, init_state=h, dfinal_state=h)
+        assert dx.shape == x.shape and not dlam.any() and torch.equal(dinit, h)
+        assert not ssd.gated_scan(x, x, x, lam)[1].any()
+
+
 def test_bad_offsets_stay_in_bounds():
     """Offsets that decrease, leave the stream or start late: no result is
     promised, but nothing outside the tensors is touched and the call ends."""
