@@ -7,12 +7,14 @@
 // A few operations per element read: HBM streams.  A row is held in
 // registers between the sum and its use, so every input is read once.
 //
-// A row (or group of a row) belongs to a team of lanes, 8 consecutive columns
-// each: 8 to 64 lanes of a wave, or all waves of a workgroup where it is wider.
+// A row (or group of a row) belongs to a team of lanes, 8 columns each at a time:
+// 8 to 64 lanes of a wave, or all waves of a workgroup where it is wider.
 // Wide rows over many waves with few registers a lane beat one wave with many
 // (65536 rows of 2560 columns, forward and backward: 5 waves a row and the
 // next row in flight 974 us, one wave a row 1069 us; 256 rows forward 4.2
-// against 5.8 us), and narrow groups share a wave.
+// against 5.8 us), and narrow groups share a wave.  Now: those rows, with an
+// fp32 residual, 922 us, 5.5 TB/s; 49152 rows of 8192 columns in 8 groups,
+// gated, forward and backward 1160 us, 5.5 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -29,17 +31,39 @@ constexpr int64_t kMaxBlocks = 1 << 22;  // a launch counts its lanes in 32 bits
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Eight consecutive elements as loaded.  The data is read and written once:
-// bf16, 16 bytes a lane and whole lines a wave, streams past the caches
-// (49152 rows of 8192 columns forward and backward 1159 us, cached 1180 us);
-// fp32 takes two accesses that share every line and needs the cache between
-// them (974 us cached, 1037 us streamed).
-template <typename T>
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// A lane's 8 columns are consecutive, 16 bytes of bf16 and whole lines a wave,
+// which stream past the caches (the data is read and written once; 49152 rows of
+// 8192 columns forward and backward 1159 us, cached 1180 us).  fp32 takes two
+// accesses that share every line, and so needs the cache between them.  SPLIT,
+// the residual norm where a type is fp32: two times 4 consecutive columns, half
+// a team's width apart, so that fp32 too is streamed in whole lines (65536 rows of
+// 2560 columns with an fp32 residual 921 us, consecutive and cached 967 us; the
+// gated norm, with one fp32 tensor in five, loses by it: 358 against 350 us for
+// 16384 rows of 5120).
+struct Cols {
+    int c[2];
+    bool on[2];
+};
+
+template <typename T, bool SPLIT>
 struct Eight;
-template <>
-struct Eight<bf16_t> {
+template <bool SPLIT>
+struct Eight<bf16_t, SPLIT> {
     typedef u32x4 raw;
-    __device__ static inline raw load(const bf16_t* p) { return __builtin_nontemporal_load((const raw*)p); }
+    __device__ static inline raw load(const bf16_t* p, const Cols& k) {
+        raw r = {};
+        if constexpr (!SPLIT) {
+            if (k.on[0]) r = __builtin_nontemporal_load((const raw*)(p + k.c[0]));
+        } else {
+            u32x2 lo = {}, hi = {};
+            if (k.on[0]) lo = __builtin_nontemporal_load((const u32x2*)(p + k.c[0]));
+            if (k.on[1]) hi = __builtin_nontemporal_load((const u32x2*)(p + k.c[1]));
+            r = raw{lo[0], lo[1], hi[0], hi[1]};
+        }
+        return r;
+    }
     __device__ static inline f32x8 widen(raw v) {
         f32x8 r;
 #pragma unroll
@@ -49,19 +73,44 @@ struct Eight<bf16_t> {
         }
         return r;
     }
-    __device__ static inline void store(bf16_t* p, f32x8 v) {
-        __builtin_nontemporal_store(Tr<bf16_t>::narrow(v), (bf16x8*)p);
+    __device__ static inline void store(bf16_t* p, const Cols& k, f32x8 v) {
+        const bf16x8 n = Tr<bf16_t>::narrow(v);
+        if constexpr (!SPLIT) {
+            if (k.on[0]) __builtin_nontemporal_store(n, (bf16x8*)(p + k.c[0]));
+        } else {
+            if (k.on[0]) __builtin_nontemporal_store(__builtin_shufflevector(n, n, 0, 1, 2, 3), (bf16x4*)(p + k.c[0]));
+            if (k.on[1]) __builtin_nontemporal_store(__builtin_shufflevector(n, n, 4, 5, 6, 7), (bf16x4*)(p + k.c[1]));
+        }
     }
 };
-template <>
-struct Eight<float> {
+template <bool SPLIT>
+struct Eight<float, SPLIT> {
     typedef f32x8 raw;
-    __device__ static inline raw load(const float* p) {
-        return Tr<float>::ld8(p);
+    __device__ static inline const float* second(const float* p, const Cols& k) { return p + (SPLIT ? k.c[1] : k.c[0] + 4); }
+    __device__ static inline bool has_second(const Cols& k) { return k.on[SPLIT ? 1 : 0]; }
+    __device__ static inline raw load(const float* p, const Cols& k) {
+        if constexpr (!SPLIT) return cached(p, k);
+        f32x4 lo = {}, hi = {};
+        if (k.on[0]) lo = __builtin_nontemporal_load((const f32x4*)(p + k.c[0]));
+        if (k.on[1]) hi = __builtin_nontemporal_load((const f32x4*)(p + k.c[1]));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // weights, and what is summed over rows
+    __device__ static inline raw cached(const float* p, const Cols& k) {
+        f32x4 lo = {}, hi = {};
+        if (k.on[0]) lo = *(const f32x4*)(p + k.c[0]);
+        if (has_second(k)) hi = *(const f32x4*)second(p, k);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     __device__ static inline f32x8 widen(raw v) { return v; }
-    __device__ static inline void store(float* p, f32x8 v) {
-        Tr<float>::st8(p, v);
+    __device__ static inline void store(float* p, const Cols& k, f32x8 v) {
+        if constexpr (!SPLIT) return store_cached(p, k, v);
+        if (k.on[0]) __builtin_nontemporal_store(__builtin_shufflevector(v, v, 0, 1, 2, 3), (f32x4*)(p + k.c[0]));
+        if (k.on[1]) __builtin_nontemporal_store(__builtin_shufflevector(v, v, 4, 5, 6, 7), (f32x4*)(p + k.c[1]));
+    }
+    __device__ static inline void store_cached(float* p, const Cols& k, f32x8 v) {
+        if (k.on[0]) *(f32x4*)(p + k.c[0]) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+        if (has_second(k)) *(f32x4*)second(p, k) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
     }
 };
 
@@ -91,7 +140,16 @@ struct Team {
         index = (int64_t)blockIdx.x * per + (WIDE ? 0 : (int)threadIdx.x / LANES);
         teams = (int64_t)gridDim.x * per;
     }
-    __device__ int col(int v) const { return v * stride + lane * kVec; }
+    // The lane's columns of its v-th vector, and whether a row of n columns has them.
+    template <bool SPLIT>
+    __device__ Cols cols(int v, int n) const {
+        Cols k;
+        k.c[0] = v * stride + lane * (SPLIT ? 4 : kVec);
+        k.c[1] = k.c[0] + (SPLIT ? stride / 2 : 0);
+        k.on[0] = k.c[0] < n;
+        k.on[1] = k.c[1] < n;
+        return k;
+    }
     // Sum over the team, the same in every lane.
     __device__ float sum(float v, float* lds) const {
 #pragma unroll
@@ -113,6 +171,10 @@ struct Team {
 template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
 __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void norm_forward_kernel(NormArgs a) {
     __shared__ float lds[kMaxWaves];
+    constexpr bool SPLIT = KIND == 0 && (sizeof(A) == 4 || sizeof(B) == 4);
+    typedef Eight<A, SPLIT> EA;
+    typedef Eight<B, SPLIT> EB;
+    typedef Eight<float, SPLIT> EW;
     const Team<LANES, WIDE, V> p;
     const int n = a.D / a.G;
     const int64_t segs = a.rows * a.G;
@@ -125,30 +187,23 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void norm_forward_kern
         const int g0 = on ? (int)(seg - row * a.G) * n : 0;
         const A* xa = KIND == 0 ? (const A*)a.x + row * a.x_stride + g0 : (const A*)a.z + row * a.z_stride + g0;
         const B* xb = KIND == 0 ? (const B*)a.z + row * a.z_stride + g0 : (const B*)a.x + row * a.x_stride + g0;
-        typename Eight<A>::raw ra[V];
-        typename Eight<B>::raw rb[V];
+        typename EA::raw ra[V];
+        typename EB::raw rb[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = p.col(v);
-            ra[v] = {};
-            rb[v] = {};
-            if (on && c < n) {
-                ra[v] = Eight<A>::load(xa + c);
-                rb[v] = Eight<B>::load(xb + c);
-            }
+            const Cols k = p.template cols<SPLIT>(v, on ? n : 0);
+            ra[v] = EA::load(xa, k);
+            rb[v] = EB::load(xb, k);
         }
         f32x8 u[V], gate[V];
         float ss = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = p.col(v);
-            const f32x8 va = Eight<A>::widen(ra[v]), vb = Eight<B>::widen(rb[v]);
+            const Cols k = p.template cols<SPLIT>(v, on ? n : 0);
+            const f32x8 va = EA::widen(ra[v]), vb = EB::widen(rb[v]);
             if constexpr (KIND == 0) {
-                u[v] = vb + va;
-                if (on && c < n) {
-                    if (a.scale) u[v] = vb + Tr<float>::ld8(a.scale + g0 + c) * va;
-                    Eight<B>::store((B*)a.out + row * a.D + g0 + c, u[v]);
-                }
+                u[v] = a.scale ? vb + EW::cached(a.scale + g0, k) * va : vb + va;
+                EB::store((B*)a.out + row * a.D + g0, k, u[v]);
             } else {
                 gate[v] = silu8(va);
                 u[v] = KIND == 1 ? vb * gate[v] : vb;
@@ -160,12 +215,10 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void norm_forward_kern
         if (a.rstd && p.lane == 0) a.rstd[seg] = rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = p.col(v);
-            if (c < n) {
-                f32x8 y = u[v] * rstd * Tr<float>::ld8(a.weight + g0 + c);
-                if constexpr (KIND == 2) y *= gate[v];
-                Eight<A>::store((A*)a.y + row * a.D + g0 + c, y);
-            }
+            const Cols k = p.template cols<SPLIT>(v, n);
+            f32x8 y = u[v] * rstd * EW::cached(a.weight + g0, k);
+            if constexpr (KIND == 2) y *= gate[v];
+            EA::store((A*)a.y + row * a.D + g0, k, y);
         }
     }
 }
@@ -180,13 +233,17 @@ template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
 __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void norm_backward_kernel(NormArgs a) {
     __shared__ float lds[kMaxWaves];
     __shared__ f32x4 sums[WIDE ? 1 : 3 * 64 * V * 2];
+    constexpr bool SPLIT = KIND == 0 && (sizeof(A) == 4 || sizeof(B) == 4);
+    typedef Eight<A, SPLIT> EA;
+    typedef Eight<B, SPLIT> EB;
+    typedef Eight<float, SPLIT> EW;
     const Team<LANES, WIDE, V> p;
     const int n = a.D / a.G, g0 = blockIdx.y * n;
     const bool scaled = KIND == 0 && a.dscale;
     // KIND 0: dy, the new residual, its gradient, x;  else: dy, x, z
     struct Row {
-        typename Eight<A>::raw dy[V], za[V];
-        typename Eight<B>::raw xb[V], db[V];
+        typename EA::raw dy[V], za[V];
+        typename EB::raw xb[V], db[V];
         float rstd;
     };
     auto load = [&](int64_t row, Row& r) {
@@ -194,27 +251,27 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void n
         r.rstd = there ? a.rstd_in[row * a.G + blockIdx.y] : 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = p.col(v);
-            r.dy[v] = r.za[v] = {};
-            r.xb[v] = r.db[v] = {};
-            if (!there || c >= n) continue;
-            const int64_t dense = row * a.D + g0 + c;
-            r.dy[v] = Eight<A>::load((const A*)a.dy + dense);
+            const Cols k = p.template cols<SPLIT>(v, there ? n : 0);
+            const int64_t dense = row * a.D + g0;
+            r.dy[v] = EA::load((const A*)a.dy + dense, k);
             if constexpr (KIND == 0) {
-                r.xb[v] = Eight<B>::load((const B*)a.out + dense);
-                if (a.dout) r.db[v] = Eight<B>::load((const B*)a.dout + dense);
-                if (scaled) r.za[v] = Eight<A>::load((const A*)a.x + row * a.x_stride + g0 + c);
+                r.xb[v] = EB::load((const B*)a.out + dense, k);
+                r.za[v] = {};
+                r.db[v] = {};
+                if (a.dout) r.db[v] = EB::load((const B*)a.dout + dense, k);
+                if (scaled) r.za[v] = EA::load((const A*)a.x + row * a.x_stride + g0, k);
             } else {
-                r.xb[v] = Eight<B>::load((const B*)a.x + row * a.x_stride + g0 + c);
-                r.za[v] = Eight<A>::load((const A*)a.z + row * a.z_stride + g0 + c);
+                r.xb[v] = EB::load((const B*)a.x + row * a.x_stride + g0, k);
+                r.za[v] = EA::load((const A*)a.z + row * a.z_stride + g0, k);
             }
         }
     };
     f32x8 w[V], sc[V], dw[V] = {}, ds[V] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        w[v] = p.col(v) < n ? Tr<float>::ld8(a.weight + g0 + p.col(v)) : f32x8{};
-        if (KIND == 0) sc[v] = a.scale && p.col(v) < n ? Tr<float>::ld8(a.scale + g0 + p.col(v)) : f32x8{1, 1, 1, 1, 1, 1, 1, 1};
+        const Cols k = p.template cols<SPLIT>(v, n);
+        w[v] = EW::cached(a.weight + g0, k);
+        if (KIND == 0) sc[v] = a.scale ? EW::cached(a.scale + g0, k) : f32x8{1, 1, 1, 1, 1, 1, 1, 1};
     }
     constexpr bool kAhead = V < 4;  // there are no registers for the next row of the widest ones
     Row cur, nxt;
@@ -233,12 +290,12 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void n
         float dot = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            f32x8 d = Eight<A>::widen(cur.dy[v]);
-            const f32x8 xb = Eight<B>::widen(cur.xb[v]);
+            f32x8 d = EA::widen(cur.dy[v]);
+            const f32x8 xb = EB::widen(cur.xb[v]);
             if constexpr (KIND == 0) {
                 m[v] = xb * cur.rstd;
             } else {
-                const f32x8 gate = silu8(Eight<A>::widen(cur.za[v]));
+                const f32x8 gate = silu8(EA::widen(cur.za[v]));
                 m[v] = (KIND == 1 ? xb * gate : xb) * cur.rstd;
                 if (KIND == 2) d *= gate;
             }
@@ -250,17 +307,16 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void n
         if (row >= a.rows) continue;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = p.col(v);
-            if (c >= n) continue;
+            const Cols k = p.template cols<SPLIT>(v, n);
             f32x8 dv = (wd[v] - m[v] * mean) * cur.rstd;
             if constexpr (KIND == 0) {
-                dv += Eight<B>::widen(cur.db[v]);
-                const int64_t dense = row * a.D + g0 + c;
-                if (a.dz) Eight<B>::store((B*)a.dz + dense, dv);
-                if (scaled) ds[v] += dv * Eight<A>::widen(cur.za[v]);
-                Eight<A>::store((A*)a.dx + dense, dv * sc[v]);
+                dv += EB::widen(cur.db[v]);
+                const int64_t dense = row * a.D + g0;
+                if (a.dz) EB::store((B*)a.dz + dense, k, dv);
+                if (scaled) ds[v] += dv * EA::widen(cur.za[v]);
+                EA::store((A*)a.dx + dense, k, dv * sc[v]);
             } else {
-                const f32x8 zv = Eight<A>::widen(cur.za[v]), xv = Eight<B>::widen(cur.xb[v]), dy = Eight<A>::widen(cur.dy[v]);
+                const f32x8 zv = EA::widen(cur.za[v]), xv = EB::widen(cur.xb[v]), dy = EA::widen(cur.dy[v]);
                 f32x8 dx, dz;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -273,8 +329,8 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void n
                         dz[e] = dy[e] * w[v][e] * m[v][e] * dsilu;
                     }
                 }
-                Eight<B>::store((B*)a.dx + row * a.dx_stride + g0 + c, dx);
-                Eight<A>::store((A*)a.dz + row * a.dz_stride + g0 + c, dz);
+                EB::store((B*)a.dx + row * a.dx_stride + g0, k, dx);
+                EA::store((A*)a.dz + row * a.dz_stride + g0, k, dz);
             }
         }
     }
@@ -312,8 +368,7 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void n
                 }
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (p.col(v) < n) Tr<float>::st8(to + p.col(v), s[v]);
+        for (int v = 0; v < V; ++v) EW::store_cached(to, p.template cols<SPLIT>(v, n), s[v]);
     }
 }
 
