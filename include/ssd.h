@@ -462,8 +462,10 @@ ssd_status ssd_gated_scan_workspace_size(const ssd_gated_shape* shape, int32_t b
  *   final_state  [batch, C]     fp32, or NULL (not written); not init_state
  *   states       [states_rows, C] fp32, or NULL (not written)
  *   workspace    device scratch of the queried size, 16-byte aligned,
- *                contents undefined on entry and exit
+ *                contents undefined on entry and exit; calls that may overlap
+ *                need workspaces of their own
  * No output may alias an input or another output.
+ * Results do not depend on timing: the same call gives the same bits.
  * Errors: SSD_ERR_NULL, SSD_ERR_ALIGN, SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes,
  * strides, aliasing), SSD_ERR_VALUE (rate), SSD_ERR_SEQLENS,
  * SSD_ERR_WORKSPACE, SSD_ERR_HIP.

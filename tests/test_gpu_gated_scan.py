@@ -120,6 +120,7 @@ PACKED = [
     ([2500, 2049, 1], 72, "f32", 200),
     ([0, 0], 8, "f32", 0),
     ([0], 8, "bf16", 5),
+    ([3001, 0, 5197], 1032, "bf16", 0),  # more than a round of workgroups, tiles no multiple of 8
 ]
 
 
