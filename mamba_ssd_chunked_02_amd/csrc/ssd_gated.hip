@@ -49,6 +49,8 @@ constexpr int kGroup = 8;                       // tiles per group of the carry
 constexpr int kBitRows = 8;                     // rows per word of boundary bits
 constexpr int kFwdRows = 8, kBwdRows = 4;       // rows per run (per lane)
 constexpr uint64_t kNotYet = ~(uint64_t)0;      // a published word that is not there yet
+static_assert(kFwdTile % kGatedStateRows == 0 && kGatedStateRows % kFwdRows == 0 && kBitRows % kFwdRows == 0 &&
+              kBitRows % kBwdRows == 0, "saved states and boundary words fall on runs");
 
 __device__ inline bool is_reset(float P) { return __builtin_bit_cast(int, P) < 0; }
 
@@ -358,6 +360,7 @@ __device__ inline float enter_tile(const GatedPass& ps, int64_t ord, int chan, i
     uint64_t e = wave == 0 && g > 0 ? look(ps.entry + g * C + at) : 0;
     // the maps of the group's earlier tiles: wave w takes kGroup / WAVES of them
     constexpr int kEach = kGroup / WAVES;
+    static_assert(kEach * WAVES == kGroup && WAVES >= 2, "every wave takes as many maps");
     const int j0 = wave * kEach;
     if (j0 < p) {
         const uint64_t* m = ps.maps + (g * kGroup + j0) * C + at;
