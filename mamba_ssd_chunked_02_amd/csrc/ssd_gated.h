@@ -1,46 +1,13 @@
-// Shared by the gated recurrence's kernels: the sequence boundaries inside a
-// run of rows, and the gates of one element.
+// Shared by the gated recurrence's kernels and the conv1d gradients: four
+// channels as they are loaded, and the gates of one element.
 #pragma once
 
 #include "ssd_device.h"
+#include "ssd_rows.h"
 
 namespace ssd {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// ---------------------------------------------------------------- rows
-// Offsets are clamped into [0, T] with the end no earlier than the start, so
-// no row or state index derived from them leaves its array, whatever the
-// device list holds.
-struct RowRange {
-    int64_t lo, hi;
-};
-
-__device__ inline RowRange seq_range(const int32_t* cu, int64_t L, int64_t T, int64_t s) {
-    if (!cu) return {s * L, s * L + L};
-    const int64_t lo = min(max((int64_t)cu[s], (int64_t)0), T);
-    return {lo, min(max((int64_t)cu[s + 1], lo), T)};
-}
-
-// Rows that belong to sequences.  Rows outside (behind the last sequence) are
-// neither read into a result nor written.
-__device__ inline RowRange live_rows(const int32_t* cu, int64_t nseq, int64_t T) {
-    if (!cu) return {0, T};
-    const int64_t lo = min(max((int64_t)cu[0], (int64_t)0), T);
-    return {lo, min(max((int64_t)cu[nseq], lo), T)};
-}
-
-// The sequence holding a live row: the last one that starts at or before it.
-__device__ inline int64_t seq_of(const int32_t* cu, int64_t nseq, int64_t L, int64_t row) {
-    if (!cu) return (uint32_t)row / (uint32_t)L;  // rows < 2^31
-    int64_t lo = 0, hi = nseq - 1;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= row) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
 
 // ---------------------------------------------------------------- four channels as loaded
 // bf16 channels stay in the two words they were loaded as (a vector of 16-bit

@@ -46,11 +46,9 @@ constexpr int kSegLanes = 16;                   // lanes across the channels of 
 constexpr int kTileCh = kLaneCh * kSegLanes;    // channels per workgroup
 constexpr int kFwdTile = 128, kBwdTile = kGatedStateRows;  // rows per tile
 constexpr int kGroup = 8;                       // tiles per group of the carry
-constexpr int kBitRows = 8;                     // rows per word of boundary bits
 constexpr int kFwdRows = 8, kBwdRows = 4;       // rows per run (per lane)
 constexpr uint64_t kNotYet = ~(uint64_t)0;      // a published word that is not there yet
-static_assert(kFwdTile % kGatedStateRows == 0 && kGatedStateRows % kFwdRows == 0 && kBitRows % kFwdRows == 0 &&
-              kBitRows % kBwdRows == 0, "saved states and boundary words fall on runs");
+static_assert(kFwdTile % kGatedStateRows == 0 && kGatedStateRows % kFwdRows == 0, "saved states fall on runs");
 
 __device__ inline bool is_reset(float P) { return __builtin_bit_cast(int, P) < 0; }
 
@@ -76,23 +74,6 @@ __device__ inline bool there(uint64_t v) { return (uint32_t)(v >> 32) != 0xfffff
 __device__ inline float hi_of(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)(v >> 32)); }
 __device__ inline float lo_of(uint64_t v) { return __builtin_bit_cast(float, (uint32_t)v); }
 
-// Boundary bits of ROWS rows from t0 (a multiple of ROWS): bit j: row t0 + j is
-// its sequence's first one; bit 16 + j: its last one.
-template <int ROWS>
-__device__ inline uint32_t boundary_bits(const GatedArgs& a, int64_t t0) {
-    if (a.cu) {
-        const uint32_t w = a.bits[t0 / kBitRows] >> (t0 % kBitRows);
-        return w & (((1u << ROWS) - 1) * 0x10001u);
-    }
-    uint32_t m = 0;
-    const uint32_t p = (uint32_t)t0 % (uint32_t)a.L;  // rows < 2^31
-    for (int64_t j = p ? a.L - p : 0; j <= ROWS; j += a.L) {
-        if (j < ROWS) m |= 1u << j;
-        if (j > 0) m |= 1u << (15 + j);
-    }
-    return m;
-}
-
 // Before the pass: the published words set to kNotYet and the counters to 0;
 // for a packed batch the boundary bits, and the states of sequences without
 // tokens (their state passes through: out = in).
@@ -103,25 +84,8 @@ __global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, GatedPlan 
     for (int64_t k = me; k < pl.ncounters; k += stride) pl.counters[k] = 0;
     const int64_t nruns = (a.T + kBitRows - 1) / kBitRows;
     const RowRange live = live_rows(a.cu, a.nseq, a.T);
-    for (int64_t k = me; pl.bits && k < nruns; k += stride) {
-        const int64_t t0 = k * kBitRows, t1 = min(t0 + kBitRows, live.hi);
-        uint32_t m = 0;
-        // every offset in [t0, t1] ends a sequence at the row before it and starts one at its row
-        for (int64_t t = max(t0, live.lo); t <= t1;) {
-            int64_t lo = 0, hi = a.nseq;  // the first offset >= t
-            while (lo < hi) {
-                const int64_t mid = (lo + hi) >> 1;
-                if (a.cu[mid] < t) lo = mid + 1;
-                else hi = mid;
-            }
-            const int64_t at = max((int64_t)a.cu[lo], t);
-            if (at > t1) break;
-            if (at < t1) m |= 1u << (at - t0);
-            if (at > t0) m |= 1u << (15 + at - t0);
-            t = at + 1;
-        }
-        pl.bits[k] = m;
-    }
+    for (int64_t k = me; pl.bits && k < nruns; k += stride)
+        pl.bits[k] = packed_boundaries(a.cu, a.nseq, live, k * kBitRows);
     if (!pl.out) return;
     const int64_t waves = stride / 64, lane = me & 63;
     for (int64_t s = me / 64; s < a.nseq; s += waves) {
@@ -131,8 +95,8 @@ __global__ __launch_bounds__(256) void gated_plan_kernel(GatedArgs a, GatedPlan 
     }
 }
 
-// What a lane has of its run of rows: the place, the boundary bits and the
-// live rows (bit j).  plain: no run of the wave has a boundary or a row that is
+// What a lane has of its run of rows: the place, the boundary bits (of live rows)
+// and the live rows (bit j).  plain: no run of the wave has a boundary or a row that is
 // not live, and so none of the tests per row is needed.
 template <int ROWS, int TILE>
 struct Run {
@@ -146,8 +110,8 @@ struct Run {
     __device__ bool start(int j) const { return bits >> j & 1; }
     __device__ bool end(int j) const { return bits >> (16 + j) & 1; }
     __device__ bool has(int j) const { return live >> j & 1; }
-    __device__ bool any_start() const { return bits & live; }
-    __device__ bool any_end() const { return bits >> 16 & live; }
+    __device__ bool any_start() const { return bits & 0xffff; }
+    __device__ bool any_end() const { return bits >> 16; }
 
     __device__ Run(const GatedArgs& a, int64_t tile, int cb) {
         tile0 = tile * TILE;
@@ -165,11 +129,9 @@ struct Run {
                 return;
             }
         }
-        bits = t(0) < a.T ? boundary_bits<ROWS>(a, t(0)) : 0;
-        const RowRange r = live_rows(a.cu, a.nseq, a.T);
-        const int lo = (int)min(max(r.lo - t(0), (int64_t)0), (int64_t)ROWS);
-        const int hi = (int)min(max(r.hi - t(0), (int64_t)lo), (int64_t)ROWS);
-        live = ((1u << hi) - 1) & ~((1u << lo) - 1);
+        const RunBits r = run_bits<ROWS>(a.cu, a.bits, a.nseq, a.L, a.T, t(0));
+        bits = r.bits;
+        live = r.live;
         plain = __builtin_amdgcn_readfirstlane(__all(bits == 0 && live == (1u << ROWS) - 1));
     }
 };
