@@ -421,7 +421,7 @@ ssd_status ssd_causal_conv1d_backward(const ssd_conv_outputs* dout, const void* 
  *   channels     C, a multiple of 8, at most 2^20
  *   dtype        ssd_dtype of x, r, i (and dx, dr, di)
  *   ydtype       ssd_dtype of y (and dy)
- *   rate         finite and > 0
+ *   rate         finite and > 0; rate softplus(lam[c]) counts as at most 1e30
  *   x_stride, r_stride, i_stride      elements from one row to the next:
  *                multiples of 8, in [C, 2^22]; 0 means C
  *   dx_stride, dr_stride, di_stride   the same for the gradients (backward only)

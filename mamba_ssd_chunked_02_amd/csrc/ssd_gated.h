@@ -61,11 +61,13 @@ __device__ inline float softplus_f(float v) {
     return v < -87.f ? 0.f : fmaxf(v, 0.f) + s * p;
 }
 
-// The factor of sigmoid(r) in log a: -rate softplus(lam), no lower than -1e4
-// (exp of which is 0) so that sums of it stay finite; NaN stays NaN.
+// The factor of sigmoid(r) in log a: -rate softplus(lam).  However large it is, a
+// gate that is nearly closed makes a decay of it that counts, so nothing may be
+// cut off before the gate has multiplied it but what keeps it finite (a gate of 0
+// times infinity is no number): no lower than -1e30.  NaN stays NaN.
 __device__ inline float decay_factor(float lam, float rate) {
     const float k = -rate * softplus_f(lam);
-    return k < -1e4f ? -1e4f : k;
+    return k < -1e30f ? -1e30f : k;
 }
 
 // exp(v) - 1 for v in [-0.35, 0]: v times the minimax polynomial of degree 4 of
@@ -83,8 +85,15 @@ __device__ inline float expm1_slow(float v) {
 
 // a = exp(v) and m = 1 - a^2 = -e (1 + a), e = a - 1, with no cancellation
 // however near a is to 1, and w, which holds both: e (<= 0) where v >= -0.35,
-// elsewhere a itself (> 0).  slow (the same for a wave): no channel of the wave
+// elsewhere a itself, no less than kLeastDecay (> 0), which is taken off again where
+// w is read: a gradient multiplies an a that underflowed by the decay factor, which
+// may be 1e30, and has to find 0.  slow (the same for a wave): no channel of the wave
 // decays by more than 0.35 a token, so that no element takes the exponential.
+constexpr float kLeastDecay = 1e-37f;
+
+// a of one held decay; what is taken off is below half a step of any a over 2e-30.
+__device__ inline float held_decay(float held) { return held + (held > 0.f ? -kLeastDecay : 1.f); }
+
 struct Decay {
     f32x4 a, m, w;
     __device__ inline void from_log(f32x4 v, bool slow) {
@@ -98,8 +107,8 @@ struct Decay {
         } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                // the floor keeps w > 0 where a underflows
-                const float p = expm1_slow(v[c]), q = fmaxf(__builtin_amdgcn_exp2f(v[c] * 1.44269504088896341f), 1e-37f);
+                const float p = expm1_slow(v[c]),
+                            q = fmaxf(__builtin_amdgcn_exp2f(v[c] * 1.44269504088896341f), kLeastDecay);
                 const bool far = v[c] < kSlowDecay;
                 const float e = far ? q - 1.f : p;
                 a[c] = far ? q : 1.f + p;
@@ -119,7 +128,7 @@ struct Decay {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float e = held[c] > 0.f ? held[c] - 1.f : held[c];
-                a[c] = held[c] > 0.f ? held[c] : 1.f + held[c];
+                a[c] = held_decay(held[c]);
                 m[c] = __builtin_fmaf(-e, a[c], -e);
             }
         }
@@ -134,7 +143,7 @@ __device__ inline f32x4 decay_of(f32x4 held, bool slow) {
         for (int c = 0; c < 4; ++c) a[c] = 1.f + held[c];
     } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) a[c] = held[c] > 0.f ? held[c] : 1.f + held[c];
+        for (int c = 0; c < 4; ++c) a[c] = held_decay(held[c]);
     }
     return a;
 }
