@@ -527,6 +527,9 @@ ssd_status ssd_gated_scan_step(const float* state, float* state_out, const void*
  *                and their gradients in elements (multiples of 8, at least D; 0
  *                means D); 0 for the residual norm
  *   reserved     must be 0
+ * No output may alias an input or another output, but for the one in place of
+ * one input that is named below (and with it of the inputs of its type and
+ * shape that are that same tensor).
  */
 typedef struct ssd_norm_shape {
     int64_t rows;

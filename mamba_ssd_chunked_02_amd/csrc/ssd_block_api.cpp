@@ -31,9 +31,15 @@ struct Arg {
     bool output;
 };
 
+// One output that may be the same tensor as some inputs (bits of their places
+// in the list of arguments); no other output may.
+struct InPlace {
+    int output;
+    uint32_t inputs;
+};
+
 // NULLs, 16-byte alignment, and outputs that are an input or another output.
-// `shared`: one pair (output, input) that may be the same tensor.
-ssd_status check_args(const Arg* args, int n, const void* shared = nullptr) {
+ssd_status check_args(const Arg* args, int n, InPlace in_place = {-1, 0}) {
     for (int i = 0; i < n; ++i) {
         if (!args[i].p) {
             if (args[i].required) FAIL(SSD_ERR_NULL, "%s is NULL", args[i].name);
@@ -42,9 +48,11 @@ ssd_status check_args(const Arg* args, int n, const void* shared = nullptr) {
         if ((uintptr_t)args[i].p & 15u) FAIL(SSD_ERR_ALIGN, "%s is not 16-byte aligned", args[i].name);
     }
     for (int i = 0; i < n; ++i) {
-        if (!args[i].p || !args[i].output || args[i].p == shared) continue;
-        for (int j = 0; j < n; ++j)
-            if (j != i && args[j].p == args[i].p) FAIL(SSD_ERR_SHAPE, "%s aliases %s", args[i].name, args[j].name);
+        if (!args[i].p || !args[i].output) continue;
+        for (int j = 0; j < n; ++j) {
+            if (j == i || args[j].p != args[i].p || (i == in_place.output && in_place.inputs >> j & 1)) continue;
+            FAIL(SSD_ERR_SHAPE, "%s aliases %s", args[i].name, args[j].name);
+        }
     }
     return SSD_OK;
 }
@@ -323,7 +331,7 @@ SSD_API ssd_status ssd_gated_scan_step(const float* state, float* state_out, con
                         {i, "i", any, false},        {lam, "lam", true, false},
                         {state, "state", any, false}, {y, "y", any, true},
                         {state_out, "state_out", any, true}};
-    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])), state_out == state ? state : nullptr);
+    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])), {6, 1u << 4});
     if (st != SSD_OK) return st;
     a.x = x;
     a.r = r;
@@ -402,7 +410,10 @@ SSD_API ssd_status ssd_add_rms_norm(const void* x, const void* residual, const f
                         {weight, "weight", true, false}, {scale, "scale", false, false},
                         {y, "y", any, true},          {out, "out", any, true},
                         {rstd, "rstd", false, true}};
-    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])), out == residual ? out : nullptr);
+    // a lane reads its elements of x and the residual before it writes out; x may be the residual
+    const bool in_place = out == residual;
+    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])),
+                    {in_place ? 5 : -1, 1u << 1 | (a.a_f32 == a.b_f32 ? 1u << 0 : 0)});
     if (st != SSD_OK) return st;
     a.x = x;
     a.z = residual;
@@ -435,10 +446,11 @@ SSD_API ssd_status ssd_add_rms_norm_backward(const void* dy, const void* dout, c
                         {dresidual, "dresidual", false, true},
                         {dweight, "dweight", true, true},
                         {dscale, "dscale", false, true}};
-    if (dx && dx == dresidual) FAIL(SSD_ERR_SHAPE, "dx aliases dresidual");
-    // every element of dout is read before the same lane writes it
-    const bool in_place = dresidual == dout || (dx == dout && a.a_f32 == a.b_f32);
-    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])), in_place ? dout : nullptr);
+    // a lane reads its elements of dout, and of dy, out and x where dout is one of them, before it writes the gradient
+    const bool one_type = a.a_f32 == a.b_f32;
+    const int in_place = !dout ? -1 : dresidual == dout ? 8 : dx == dout && one_type ? 7 : -1;
+    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])),
+                    {in_place, 1u << 1 | 1u << 2 | (one_type ? 1u << 0 | 1u << 5 : 0)});
     if (st != SSD_OK) return st;
     st = check_workspace(workspace, workspace_bytes, norm_workspace(a));
     if (st != SSD_OK) return st;
