@@ -423,7 +423,9 @@ ssd_status ssd_causal_conv1d_backward(const ssd_conv_outputs* dout, const void* 
  *   ydtype       ssd_dtype of y (and dy)
  *   rate         finite and > 0; rate softplus(lam[c]) counts as at most 1e30
  *   x_stride, r_stride, i_stride      elements from one row to the next:
- *                multiples of 8, in [C, 2^22]; 0 means C
+ *                multiples of 8, in [C, 2^22]; 0 means C.  One token per
+ *                sequence: any multiple of 8 from C on (the rows of one token
+ *                in a batch of long sequences lie a sequence apart)
  *   dx_stride, dr_stride, di_stride   the same for the gradients (backward only)
  *   reserved     must be 0
  * A packed batch may hold rows behind its last sequence (cu_seqlens[batch] <

@@ -323,8 +323,9 @@ def gated_scan_backward(dy, x, r, i, lam, states, *, rate: float = 8.0, init_sta
 
 
 def gated_scan_step(state, x, r, i, lam, *, rate: float = 8.0, state_out=None, y=None, y_dtype=None):
-    """One token per sequence: x, r, i [b, C]; ``state`` [b, C] fp32 is updated
-    in place, or left as it is and the new one written to ``state_out``.
+    """One token per sequence: x, r, i [b, C], dense or evenly spaced rows (the
+    token's slice x[:, t] of a batch); ``state`` [b, C] fp32 is updated in place,
+    or left as it is and the new one written to ``state_out``.
     Returns y [b, C], of x's dtype unless ``y_dtype`` says otherwise."""
     index = _gpu(x, r, i, lam, state, state_out, y)
     f32 = _torch().float32

@@ -224,9 +224,9 @@ ssd_status gated_shape_of(const ssd_gated_shape* sh, bool step, ssd::GatedArgs* 
     a->dtype = sh->dtype;
     a->y_f32 = sh->ydtype == SSD_F32;
     a->rate = sh->rate;
-    // offsets inside a tile of rows are 32 bits
+    // offsets inside a tile of rows are 32 bits; the step has no tiles
     for (auto& q : strides)
-        if (*q.to > (1 << 22)) FAIL(SSD_ERR_SHAPE, "%s %lld is over 2^22", q.name, (long long)*q.to);
+        if (!step && *q.to > (1 << 22)) FAIL(SSD_ERR_SHAPE, "%s %lld is over 2^22", q.name, (long long)*q.to);
     // a launch counts its lanes in 32 bits
     if (!step && ssd::gated_layout(a->T, a->C, false, false).blocks > ((int64_t)1 << 22))
         FAIL(SSD_ERR_SHAPE, "tensor too large for one launch");
