@@ -495,7 +495,8 @@ ssd_status ssd_gated_scan_backward(const void* dy, const float* dfinal_state, co
 /*
  * One token per sequence: x, r, i [batch, C]; state [batch, C] fp32 is read
  * and state_out (which may be state) written; y [batch, C] in ydtype.
- * shape->seqlen, cu_seqlens and the gradients' strides are ignored.
+ * shape->seqlen and cu_seqlens are ignored; the gradients' strides are checked,
+ * as in the calls above, and not used.
  */
 ssd_status ssd_gated_scan_step(const float* state, float* state_out, const void* x, const void* r, const void* i,
                                const float* lam, void* y, const ssd_gated_shape* shape, void* stream);
