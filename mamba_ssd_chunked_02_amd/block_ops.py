@@ -423,7 +423,10 @@ def add_rms_norm_backward(dy, residual_out, weight, rstd, *, dresidual_out=None,
 def _gated_norm_shape(x, z, weight, groups, eps, norm_before_gate):
     _shaped(x, z.shape, x.dtype, "x")
     _need(weight, x.shape[-1:], _torch().float32, "weight")
-    return _norm_shape(x, z.dtype, x.dtype, eps, groups, norm_before_gate, _row_stride(x, "x"), _row_stride(z, "z"))
+    sh = _norm_shape(x, z.dtype, x.dtype, eps, groups, norm_before_gate, _row_stride(x, "x"), _row_stride(z, "z"))
+    if sh.groups != groups:
+        raise ValueError("groups %r is out of range" % (groups,))
+    return sh
 
 
 def gated_rms_norm(x, z, weight, *, groups: int = 1, eps: float = 1e-5, norm_before_gate: bool = False, y=None,

@@ -199,3 +199,13 @@ def test_refusals_on_the_gpu():
               lambda: ssd.gated_rms_norm(rows, rows, w, groups=3), lambda: ssd.gated_rms_norm(rows, rows, w, groups=0)):
         with pytest.raises(ssd.SsdError):
             f()
+
+
+@pytest.mark.parametrize("groups", [2 ** 32 + 1, 2 ** 40 + 2, -(2 ** 32) + 1])
+def test_groups_of_more_than_32_bits(groups):
+    """Not taken for what their low 32 bits say."""
+    x, w = torch.zeros(3, 16, device="cuda"), torch.ones(16, device="cuda")
+    with pytest.raises(ValueError):
+        ssd.gated_rms_norm(x, x, w, groups=groups)
+    with pytest.raises(ValueError):
+        ssd.gated_rms_norm_backward(x, x, x, w, torch.zeros(3, 1, device="cuda"), groups=groups)
