@@ -391,7 +391,8 @@ ssd_status ssd_chunked_scan_noalloc(const void* x, const float* dt, const float*
  *                 contents undefined on entry and exit
  * Sums over tokens are fp32, in an order that depends on the shape alone.
  * Rows of a packed batch behind the last sequence (cu_seqlens[batch] < T) are
- * not read and not written; the host copy, where given, may end before T.
+ * not read into any result and not written; the host copy, where given, may end
+ * before T.
  * No output may alias an input or another output.  Errors as
  * ssd_causal_conv1d, plus SSD_ERR_WORKSPACE.
  */

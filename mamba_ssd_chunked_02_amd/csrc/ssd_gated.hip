@@ -5,7 +5,7 @@
 // and its gradients.  About 40 fp32 operations (6 of them quarter rate) and 8
 // bytes (bf16) an element: an HBM stream, with the vector ALU close behind
 // (busy 80% of the time forward).  Measured: 49152 rows of 8192 channels forward
-// 627 us, 5.1 TB/s; 65536 rows of 2560 channels forward and backward 840 us, 4.4
+// 627 us, 5.1 TB/s; 65536 rows of 2560 channels forward and backward 842 us, 4.4
 // TB/s.
 //
 // The token axis of the whole batch is cut into tiles of 128 rows (64 backward)
@@ -27,10 +27,11 @@
 // that runs already, and a tile's map is published before its workgroup waits
 // for anything.  The state entering a group waits only for earlier tiles.
 //
-// A decay near 1 is rounded to fp32 once (half of 2^-24); the factor P of a run
-// comes from the sum of its log a, so these roundings do not add up from run
-// to run over a memory of thousands of tokens.  1 - a^2 comes from a - 1, which
-// is computed by itself.
+// A decay near 1 is rounded to fp32 (half of 2^-24), but the factor P of a run of
+// rows comes from the sum of its log a and so has one such rounding, not one a
+// row.  Those of the runs do add up where the gates are constant: at |log a| =
+// 8.8e-8 a run of 8 rows a state is 2.3e-4 off after 65536 tokens, and below 2^-25
+// a run nothing decays.  1 - a^2 comes from a - 1, which is computed by itself.
 #include <algorithm>
 #include <type_traits>
 
@@ -445,8 +446,11 @@ __global__ __launch_bounds__(kFwdTile / kFwdRows * kSegLanes) void gated_forward
 // h_{t-1} is recomputed in fp32 from the state entering the tile, which the
 // forward pass kept; the adjoint is carried over the tiles in reverse order.
 // 4 rows a lane and 64-row tiles, so that 4 workgroups a compute unit wait apart
-// (8 rows a lane at half the waves 904 against 840 us); fp32 rows take more
-// registers and are quicker with 3 (103 against 114 us, 8083 rows of 776 channels).
+// (8 rows a lane at half the waves 904 against 840 us).  At the 128 registers of
+// four waves the bf16 kernel spills 3 of them (7 with fp32 dy; 16 and 32 bytes of
+// scratch a lane): 1.16 GB written for 1.04 at 65536 rows of 2560 channels, and
+// still quicker than three waves without (906 us).  fp32 rows take more (146) and are
+// quicker with 3 (103 against 114 us, 8083 rows of 776 channels).
 template <typename T, typename Y>
 __global__ __launch_bounds__(kBwdTile / kBwdRows * kSegLanes, sizeof(T) == 2 ? 4 : 3)
 void gated_backward_kernel(GatedArgs a, GatedPass ps, float* dlam_part) {

@@ -13,7 +13,7 @@
 // (65536 rows of 2560 columns, forward and backward: 5 waves a row and the
 // next row in flight 974 us, one wave a row 1069 us; 256 rows forward 4.2
 // against 5.8 us), and narrow groups share a wave.  Now: those rows, with an
-// fp32 residual, 922 us, 5.5 TB/s; 49152 rows of 8192 columns in 8 groups,
+// fp32 residual, 916 us, 5.5 TB/s; 49152 rows of 8192 columns in 8 groups,
 // gated, forward and backward 1160 us, 5.5 TB/s.
 #include <algorithm>
 #include <type_traits>
@@ -39,9 +39,11 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // accesses that share every line, and so needs the cache between them.  SPLIT,
 // the residual norm where a type is fp32: two times 4 consecutive columns, half
 // a team's width apart, so that fp32 too is streamed in whole lines (65536 rows of
-// 2560 columns with an fp32 residual 921 us, consecutive and cached 967 us; the
-// gated norm, with one fp32 tensor in five, loses by it: 358 against 350 us for
-// 16384 rows of 5120).
+// 2560 columns with an fp32 residual 921 us, consecutive and cached 967 us).  The
+// gated norm keeps to consecutive columns: with one fp32 tensor in five halves
+// lose (358 against 350 us for 16384 rows of 5120); with fp32 x and z they would
+// win forward (161 against 184 us there, 264 against 303 us for 8192 rows of 16384)
+// and win or lose 2 or 3% backward (308 against 314 us, 725 against 706 us).
 struct Cols {
     int c[2];
     bool on[2];
