@@ -503,6 +503,124 @@ ssd_status ssd_gated_scan_step(const float* state, float* state_out, const void*
                                const float* lam, void* y, const ssd_gated_shape* shape, void* stream);
 
 /*
+ * Selective scan: the recurrence of the SSD scan with a decay for every channel
+ * and state.  Per sequence, channel c (group g = c / (C/G)), state n and token t:
+ *
+ *     dt  = dt_raw[t, c], or with an activation
+ *           min(max(softplus(dt_raw[t, c] + dt_bias[c]), dt_min), dt_max)
+ *     h_t = exp(dt A[c, n]) h_{t-1} + dt x[t, c] B[t, g, n]
+ *     p   = sum_n h_t C[t, g, n] + D[c] x[t, c]
+ *     y   = p silu(z[t, c])                      (z NULL: p)
+ *
+ * It follows ssd_causal_conv1d in its block; x, z, B and C are often column
+ * ranges of that block's projections, hence the row strides.  The state
+ * [channels, dstate] is fp32.
+ *
+ * Shape:
+ *   batch, seqlen, cu_seqlens, cu_seqlens_host   dense or packed, as
+ *                ssd_conv_shape; rows < 2^31
+ *   channels     C, a multiple of 8, at most 2^20
+ *   dstate       N in [1, 64]
+ *   ngroups      G >= 1, divides C; at most 2^22 / N
+ *   dtype        ssd_dtype of x, dt, z, B, C and their gradients
+ *   ydtype       ssd_dtype of y (and dy)
+ *   *_stride     elements from one row to the next: for x, dt, z, dx, ddt and dz
+ *                multiples of 8, in [C, 2^22], 0 means C; for B, C, dB and dC in
+ *                [G N, 2^22], 0 means G N (a row is dense [G, N]).  One token
+ *                per sequence: any from these least ones on
+ *   reserved     must be 0
+ * Alignment: 16 bytes, but 4 for A, D, dt_bias and their gradients, and that of an
+ * element for B, C, dB and dC.
+ * A packed batch may hold rows behind its last sequence (cu_seqlens[batch] <
+ * seqlen): they are not read into any result and not written.  A sequence without
+ * tokens passes its state (and its gradient) through.
+ */
+typedef struct ssd_selective_shape {
+    int64_t batch;
+    int64_t seqlen;
+    int32_t channels;
+    int32_t dstate;
+    int32_t ngroups;
+    int32_t dtype;
+    int32_t ydtype;
+    int32_t reserved;
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+    int64_t dx_stride, ddt_stride, dz_stride, db_stride, dc_stride;
+    const int32_t* cu_seqlens;      /* device int32 [batch+1], or NULL (dense) */
+    const int32_t* cu_seqlens_host; /* optional host copy; validated when given */
+} ssd_selective_shape;
+
+/*
+ * Tokens between two saved states: the forward pass can keep the fp32 state
+ * entering every SSD_SELECTIVE_STATE_ROWS (R) tokens of a sequence, [count, C, N]
+ * in the library's order with count = batch max(ceil(seqlen / R), 1) for a dense
+ * batch and seqlen / R (rounded down) + batch for a packed one; the backward pass
+ * needs them.
+ */
+#define SSD_SELECTIVE_STATE_ROWS 64
+
+/* Workspace bytes of ssd_selective_scan (backward = 0) or _backward (1); may be 0. */
+ssd_status ssd_selective_scan_workspace_size(const ssd_selective_shape* shape, int32_t backward, size_t* bytes);
+
+/*
+ *   x, dt        [rows, C]      dtype
+ *   A            [C, N]         fp32
+ *   B, C         [rows, G, N]   dtype
+ *   D            [C]            fp32, or NULL (zero)
+ *   z            [rows, C]      dtype, or NULL (no gate)
+ *   act          NULL: dt as given; else the activation (its dt_bias [C] or NULL)
+ *   init_state   [batch, C, N]  fp32, or NULL (zero)
+ *   y            [rows, C]      ydtype
+ *   final_state  [batch, C, N]  fp32, or NULL (not written); not init_state
+ *   states       [count, C, N]  fp32, or NULL (not written)
+ *   workspace    device scratch of the queried size, 16-byte aligned, contents
+ *                undefined on entry and exit; calls that may overlap need
+ *                workspaces of their own
+ * No output may alias an input or another output.
+ * Results do not depend on timing: the same call gives the same bits.
+ * Errors: SSD_ERR_NULL, SSD_ERR_ALIGN, SSD_ERR_DTYPE, SSD_ERR_SHAPE (sizes,
+ * strides, aliasing), SSD_ERR_VALUE (the clamp), SSD_ERR_SEQLENS,
+ * SSD_ERR_WORKSPACE, SSD_ERR_HIP.
+ */
+ssd_status ssd_selective_scan(const void* x, const void* dt, const float* A, const void* B, const void* C,
+                              const float* D, const void* z, const ssd_dt_activation* act, const float* init_state,
+                              void* y, float* final_state, float* states, const ssd_selective_shape* shape,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of ssd_selective_scan for dy [rows, C] (ydtype) and dfinal_state
+ * [batch, C, N] fp32 (or NULL, zero):
+ *   dx, ddt      [rows, C]      dtype; ddt that of the raw step size, 0 where the
+ *                               clamp cuts
+ *   dA           [C, N]         fp32
+ *   dB, dC       [rows, G, N]   dtype
+ *   dD           [C]            fp32, or NULL (not written); needs D
+ *   dz           [rows, C]      dtype; needs z, and NULL without it
+ *   ddt_bias     [C]            fp32, or NULL (not written); needs act's dt_bias
+ *   dinit_state  [batch, C, N]  fp32, or NULL (not written); not dfinal_state
+ * The other arguments as given to the forward pass, states as written by it.
+ * Sums over tokens and channels are fp32, in an order that depends on the shape
+ * alone.  Same errors.
+ */
+ssd_status ssd_selective_scan_backward(const void* dy, const float* dfinal_state, const void* x, const void* dt,
+                                       const float* A, const void* B, const void* C, const float* D, const void* z,
+                                       const ssd_dt_activation* act, const float* init_state, const float* states,
+                                       void* dx, void* ddt, float* dA, void* dB, void* dC, float* dD, void* dz,
+                                       float* ddt_bias, float* dinit_state, const ssd_selective_shape* shape,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token per sequence: x, dt, z [batch, C], B, C [batch, G, N]; state [batch,
+ * C, N] fp32 is read and state_out (which may be state) written; y [batch, C] in
+ * ydtype.  shape->seqlen and cu_seqlens are ignored; the gradients' strides are
+ * checked and not used.
+ */
+ssd_status ssd_selective_scan_step(const float* state, float* state_out, const void* x, const void* dt,
+                                   const float* A, const void* B, const void* C, const float* D, const void* z,
+                                   const ssd_dt_activation* act, void* y, const ssd_selective_shape* shape,
+                                   void* stream);
+
+/*
  * RMS norms around a block.  A row (or each of its `groups` equal column
  * ranges) is divided by its root mean square; eps is finite and >= 0:
  *     rstd = 1 / sqrt(mean(v^2) + eps)

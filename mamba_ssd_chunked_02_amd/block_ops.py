@@ -19,7 +19,7 @@ import functools
 import math
 from typing import Optional, Sequence
 
-from . import (SSD_BF16, SSD_F32, SsdError, _conv_outputs, _ConvShape, _dtype_code_of, _expect, _torch, load)
+from . import (SSD_BF16, SSD_F32, SsdError, _conv_outputs, _ConvShape, _DtAct, _dtype_code_of, _expect, _torch, load)
 
 __all__ = ["gated_scan", "gated_scan_step", "gated_scan_backward", "add_rms_norm", "add_rms_norm_backward",
            "gated_rms_norm", "gated_rms_norm_backward", "causal_conv1d_backward", "GATED_STATE_ROWS"]
@@ -52,13 +52,19 @@ def _lib():
     if not _functions:
         vp, sz = ctypes.c_void_p, ctypes.c_size_t
         szp = ctypes.POINTER(sz)
-        gsp, nsp, csp = (ctypes.POINTER(t) for t in (_GatedShape, _NormShape, _ConvShape))
+        from .selective_ops import _SelectiveShape
+        gsp, nsp, csp, ssp = (ctypes.POINTER(t) for t in (_GatedShape, _NormShape, _ConvShape, _SelectiveShape))
+        act = ctypes.POINTER(_DtAct)
         declared = {}
         for name, args in {
                 "ssd_gated_scan_workspace_size": [gsp, ctypes.c_int32, szp],
                 "ssd_gated_scan": [vp] * 8 + [gsp, vp, sz, vp],
                 "ssd_gated_scan_backward": [vp] * 13 + [gsp, vp, sz, vp],
                 "ssd_gated_scan_step": [vp] * 7 + [gsp, vp],
+                "ssd_selective_scan_workspace_size": [ssp, ctypes.c_int32, szp],
+                "ssd_selective_scan": [vp] * 7 + [act] + [vp] * 4 + [ssp, vp, sz, vp],
+                "ssd_selective_scan_backward": [vp] * 9 + [act] + [vp] * 11 + [ssp, vp, sz, vp],
+                "ssd_selective_scan_step": [vp] * 9 + [act, vp, ssp, vp],
                 "ssd_norm_backward_workspace_size": [nsp, szp],
                 "ssd_add_rms_norm": [vp] * 7 + [nsp, vp],
                 "ssd_add_rms_norm_backward": [vp] * 11 + [nsp, vp, sz, vp],

@@ -254,6 +254,66 @@ hipError_t launch_gated_scan(const GatedArgs& a, const GatedLayout& lay, void* w
 hipError_t launch_gated_backward(const GatedArgs& a, const GatedLayout& lay, void* ws, hipStream_t stream);
 hipError_t launch_gated_step(const GatedArgs& a, const float* state, float* state_out, hipStream_t stream);
 
+// Selective scan (ssd_selective.hip, ssd_selective_bwd.hip): a decay per channel
+// and state.
+constexpr int64_t kSelStateRows = 64;  // SSD_SELECTIVE_STATE_ROWS of ssd.h
+constexpr int32_t kMaxSelStates = 64;
+
+struct SelArgs {
+    const void* x;             // [rows, C], like every tensor of rows with a row stride of its own
+    const void* dt;            // [rows, C]
+    const void* z;             // [rows, C] or NULL
+    const void* B;             // [rows, G, N]
+    const void* Cm;            // [rows, G, N]
+    const float* A;            // [C, N]
+    const float* D;            // [C] or NULL
+    const float* init;         // [nseq, C, N] or NULL (zero)
+    int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
+    const int32_t* cu;         // device [nseq+1] or NULL (dense)
+    int64_t nseq, L, T;
+    int32_t C, N, G;
+    int32_t dtype, y_f32;      // y_f32: y, or dy, is fp32
+    DtAct act;
+    void* y;                   // [rows, C], dense
+    float* final_state;        // [nseq, C, N] or NULL
+    float* states_out;         // [states, C, N] or NULL: the states entering every kSelStateRows tokens
+    // backward
+    const void* dy;            // [rows, C], dense
+    const float* states_in;    // states_out of the forward pass
+    const float* dfinal;       // [nseq, C, N] or NULL (zero)
+    void* dx;                  // [rows, C] with row strides of their own
+    void* ddt;
+    void* dz;
+    void* dB;                  // [rows, G, N]
+    void* dC;
+    int64_t dx_stride, ddt_stride, dz_stride, db_stride, dc_stride;
+    float* dA;                 // [C, N]
+    float* dD;                 // [C] or NULL
+    float* dbias;              // [C] or NULL
+    float* dinit;              // [nseq, C, N] or NULL
+};
+
+// Items the sequences are cut into, and byte offsets of the workspace regions
+// (256-byte aligned).
+struct SelLayout {
+    int64_t item;     // tokens of an item, a multiple of kSelStateRows
+    int64_t places;   // items, some of them empty
+    bool whole;       // every sequence is one item: nothing to carry
+    size_t states;    // f32 [places][C][4 NS]: state (or adjoint) an item ends with
+    size_t steps;     // f32 [places][C]: sum of its step sizes
+    size_t part_bc;   // f32 [channel blocks of a group][T][G][2 N]: sums of dB and dC (backward)
+    size_t part_a;    // f32 [places][C (N + 2)]: sums of dA, dD and dbias (backward)
+    int64_t blocks_bc;
+    size_t total;
+};
+
+SelLayout sel_layout(const SelArgs& a, bool backward);
+// Saved states, one per channel and state each.
+int64_t sel_saved_states(bool packed, int64_t nseq, int64_t L, int64_t T);
+hipError_t launch_selective_scan(const SelArgs& a, const SelLayout& lay, void* ws, hipStream_t stream);
+hipError_t launch_selective_backward(const SelArgs& a, const SelLayout& lay, void* ws, hipStream_t stream);
+hipError_t launch_selective_step(const SelArgs& a, const float* state, float* state_out, hipStream_t stream);
+
 // RMS norms (ssd_norm.hip).  A segment is one row's part that shares a norm
 // (the whole row, or one of its groups).
 struct NormArgs {

@@ -109,4 +109,55 @@ SSD_HOST_DEVICE inline RunBits run_bits(const int32_t* cu, const uint32_t* words
     return r;
 }
 
+// ---------------------------------------------------------------- items of sequences
+// The selective scan cuts a sequence into items of `item` tokens from its first
+// one.  Item j of sequence s is at place s * ceil(L / item) + j of a dense batch.
+// Packed: at floor(lo / item) + s + j, lo its first row: ceil(len / item) places
+// never reach the next sequence's, and there are floor(T / item) + nseq in all,
+// whatever the lengths.  An empty sequence has a place of its own too.
+struct SelItem {
+    int64_t seq;         // -1: no item at this place
+    int64_t lo;          // its first row
+    int64_t n;           // its tokens
+    int64_t first;       // the sequence's first row
+    int64_t index;       // its number in the sequence
+    bool last;
+};
+
+SSD_HOST_DEVICE inline int64_t sel_places(bool packed, int64_t nseq, int64_t L, int64_t T, int64_t item) {
+    return packed ? T / item + nseq : nseq * (L > 0 ? (L + item - 1) / item : 1);
+}
+// The place of a sequence's first item; lo: its first row.
+SSD_HOST_DEVICE inline int64_t sel_place(bool packed, int64_t s, int64_t lo, int64_t L, int64_t item) {
+    return packed ? lo / item + s : s * (L > 0 ? (L + item - 1) / item : 1);
+}
+
+SSD_HOST_DEVICE inline SelItem sel_item(const int32_t* cu, int64_t nseq, int64_t L, int64_t T, int64_t item,
+                                        int64_t place) {
+    SelItem e;
+    int64_t s, hi;
+    if (!cu) {
+        const int64_t per = L > 0 ? (L + item - 1) / item : 1;
+        s = place / per;
+    } else {  // the last sequence whose place is not behind it
+        int64_t a = 0, b = nseq - 1;
+        while (a < b) {
+            const int64_t mid = (a + b + 1) >> 1;
+            if (clamp_row(cu[mid], 0, T) / item + mid <= place) a = mid;
+            else b = mid - 1;
+        }
+        s = a;
+    }
+    const RowRange r = seq_range(cu, L, T, s);
+    e.seq = s;
+    e.first = r.lo;
+    e.index = place - sel_place(cu != nullptr, s, r.lo, L, item);
+    hi = r.hi;
+    e.lo = r.lo + e.index * item;
+    e.last = e.lo + item >= hi;
+    e.n = (e.last ? hi : e.lo + item) - e.lo;
+    if (e.index < 0 || (e.index > 0 && e.lo >= hi)) e.seq = -1;
+    return e;
+}
+
 }  // namespace ssd
