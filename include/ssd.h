@@ -711,6 +711,52 @@ ssd_status ssd_gated_rms_norm_backward(const void* dy, const void* x, const void
                                        const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes,
                                        void* stream);
 
+/*
+ * Layer norm, in front of a block with the residual addition of the block before
+ * and its scale per column, or by itself:
+ *     out  = residual + scale x           (scale NULL: residual + x; residual NULL: x)
+ *     mean = mean(out),  rstd = 1 / sqrt(mean((out - mean)^2) + eps)
+ *     y    = (out - mean) rstd weight + bias
+ * y, mean and rstd come from the fp32 sum, out is that sum rounded to its type.
+ * Shape: an ssd_norm_shape as for the residual norm (groups 1, strides and
+ * norm_before_gate 0); without a residual dtype2 is dtype.
+ *   x          [rows, D]  dtype
+ *   residual   [rows, D]  dtype2, or NULL; then scale and out are NULL too
+ *   weight     [D]        fp32
+ *   bias       [D]        fp32, or NULL (zero)
+ *   scale      [D]        fp32, or NULL
+ *   y          [rows, D]  dtype
+ *   out        [rows, D]  dtype2; may be residual
+ *   mean, rstd [rows]     fp32, or NULL (not written); the backward pass takes them
+ */
+ssd_status ssd_layer_norm(const void* x, const void* residual, const float* weight, const float* bias,
+                          const float* scale, void* y, void* out, float* mean, float* rstd,
+                          const ssd_norm_shape* shape, void* stream);
+
+/* Workspace bytes of the backward pass. */
+ssd_status ssd_layer_norm_backward_workspace_size(const ssd_norm_shape* shape, size_t* bytes);
+
+/*
+ * For the gradients dy of y and dout of out (dtype2, or NULL for zero), with out
+ * that of the forward pass (without a residual its x):
+ *     m = (out - mean) rstd
+ *     dresidual = dout + rstd (weight dy - mean(weight dy) - m mean(weight dy m))
+ *     dx = scale dresidual,  dweight = sum over rows of dy m,
+ *     dbias = sum over rows of dy,  dscale = sum over rows of dresidual x
+ *   dx         [rows, D]  dtype; may be dout where the two dtypes are one
+ *   dresidual  [rows, D]  dtype2, or NULL (not written: without a scale and
+ *              with one dtype dx is it); may be dout
+ *   dweight    [D] fp32
+ *   dbias      [D] fp32, or NULL (not written)
+ *   dscale     [D] fp32, or NULL (not written); needs scale and x
+ * Sums over rows are fp32, in an order that depends on the shape alone.
+ */
+ssd_status ssd_layer_norm_backward(const void* dy, const void* dout, const void* out, const float* weight,
+                                   const float* mean, const float* rstd, const void* x, const float* scale, void* dx,
+                                   void* dresidual, float* dweight, float* dbias, float* dscale,
+                                   const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Static English name of a status code. */
 const char* ssd_status_string(int32_t status);
 

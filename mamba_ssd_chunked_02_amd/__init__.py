@@ -23,7 +23,8 @@ from typing import Optional, Sequence, Tuple
 __all__ = ["chunked_scan", "chunked_scan_noalloc", "decode_step", "decode_window_step", "causal_conv1d",
            "conv1d_step", "workspace_size", "SsdError", "library_path", "load", "gated_scan", "gated_scan_step",
            "gated_scan_backward", "add_rms_norm", "add_rms_norm_backward", "gated_rms_norm",
-           "gated_rms_norm_backward", "causal_conv1d_backward", "selective_scan", "selective_scan_step",
+           "gated_rms_norm_backward", "causal_conv1d_backward", "layer_norm", "layer_norm_backward",
+           "add_layer_norm", "add_layer_norm_backward", "selective_scan", "selective_scan_step",
            "selective_scan_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -530,6 +531,7 @@ def conv1d_step(conv_state, x, weight, bias=None, *, activation: bool = True,
     return outs
 
 
-from .block_ops import (add_rms_norm, add_rms_norm_backward, causal_conv1d_backward, gated_rms_norm,  # noqa: E402
-                        gated_rms_norm_backward, gated_scan, gated_scan_backward, gated_scan_step)
+from .block_ops import (add_layer_norm, add_layer_norm_backward, add_rms_norm, add_rms_norm_backward,  # noqa: E402
+                        causal_conv1d_backward, gated_rms_norm, gated_rms_norm_backward, gated_scan,
+                        gated_scan_backward, gated_scan_step, layer_norm, layer_norm_backward)
 from .selective_ops import selective_scan, selective_scan_backward, selective_scan_step  # noqa: E402

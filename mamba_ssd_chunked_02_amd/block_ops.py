@@ -1,9 +1,10 @@
 """The operators around the scan in a trained or served block: the gated
-linear recurrence, the residual and gated RMS norms, and the gradients of the
-causal conv1d (``include/ssd.h``).
+linear recurrence, the residual and gated RMS norms, the layer norm, and the
+gradients of the causal conv1d (``include/ssd.h``).
 
     y, final = gated_scan(x, r, i, lam)                       # + gated_scan_step, gated_scan_backward
     y, residual = add_rms_norm(x, residual, weight, scale=s)  # + add_rms_norm_backward
+    y, residual = add_layer_norm(x, residual, weight, bias)   # + layer_norm, their _backward
     y = gated_rms_norm(x, z, weight)                          # + gated_rms_norm_backward
     dx, dweight, dbias, dstate = causal_conv1d_backward(dys, x, weight, bias)
 
@@ -22,7 +23,8 @@ from typing import Optional, Sequence
 from . import (SSD_BF16, SSD_F32, SsdError, _conv_outputs, _ConvShape, _DtAct, _dtype_code_of, _expect, _torch, load)
 
 __all__ = ["gated_scan", "gated_scan_step", "gated_scan_backward", "add_rms_norm", "add_rms_norm_backward",
-           "gated_rms_norm", "gated_rms_norm_backward", "causal_conv1d_backward", "GATED_STATE_ROWS"]
+           "layer_norm", "layer_norm_backward", "add_layer_norm", "add_layer_norm_backward", "gated_rms_norm",
+           "gated_rms_norm_backward", "causal_conv1d_backward", "GATED_STATE_ROWS"]
 
 GATED_STATE_ROWS = 64  # SSD_GATED_STATE_ROWS of include/ssd.h
 
@@ -68,6 +70,9 @@ def _lib():
                 "ssd_norm_backward_workspace_size": [nsp, szp],
                 "ssd_add_rms_norm": [vp] * 7 + [nsp, vp],
                 "ssd_add_rms_norm_backward": [vp] * 11 + [nsp, vp, sz, vp],
+                "ssd_layer_norm_backward_workspace_size": [nsp, szp],
+                "ssd_layer_norm": [vp] * 9 + [nsp, vp],
+                "ssd_layer_norm_backward": [vp] * 13 + [nsp, vp, sz, vp],
                 "ssd_gated_rms_norm": [vp] * 5 + [nsp, vp],
                 "ssd_gated_rms_norm_backward": [vp] * 8 + [nsp, vp, sz, vp],
                 "ssd_causal_conv1d_backward_workspace_size": [csp, szp],
@@ -118,6 +123,11 @@ def _gated_bytes(batch, seqlen, channels, packed, backward) -> int:
 @functools.lru_cache(maxsize=1024)
 def _norm_bytes(rows, columns, groups) -> int:
     return _query("ssd_norm_backward_workspace_size", ctypes.byref(_NormShape(rows, columns, groups)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_norm_bytes(rows, columns) -> int:
+    return _query("ssd_layer_norm_backward_workspace_size", ctypes.byref(_NormShape(rows, columns, 1)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -424,6 +434,109 @@ def add_rms_norm_backward(dy, residual_out, weight, rstd, *, dresidual_out=None,
             None if one else dresidual.data_ptr(), dweight.data_ptr(), _p(dscale), ref, workspace.data_ptr(),
             _bytes(workspace))
     return dx, dresidual, dweight, dscale
+
+
+def _layer_norm(x, residual, weight, bias, scale, eps, y, residual_out, want_stats):
+    index = _gpu(x, residual, weight, bias, scale, y, residual_out)
+    f32, shape, dtype = _torch().float32, x.shape, x.dtype
+    rdtype = dtype if residual is None else residual.dtype
+    _need(x, shape, dtype, "x")
+    _need(residual, shape, rdtype, "residual")
+    _need(weight, shape[-1:], f32, "weight")
+    _need(bias, shape[-1:], f32, "bias")
+    _need(scale, shape[-1:], f32, "scale")
+    _need(y, shape, dtype, "y")
+    _need(residual_out, shape, rdtype, "residual_out")
+    sh = _norm_shape(x, dtype, rdtype, eps)
+    if y is None:
+        y = _new(x, shape, dtype)
+    if residual_out is None and residual is not None:
+        residual_out = _new(x, shape, rdtype)
+    mean, rstd = (_new(x, shape[:-1], f32), _new(x, shape[:-1], f32)) if want_stats else (None, None)
+    _launch(index, "ssd_layer_norm", x.data_ptr(), _p(residual), weight.data_ptr(), _p(bias), _p(scale), y.data_ptr(),
+            _p(residual_out), _p(mean), _p(rstd), ctypes.byref(sh))
+    return y, residual_out, mean, rstd
+
+
+def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, y=None, want_stats: bool = False):
+    """Layer norm over the last dimension: y = (x - mean) / sqrt(var + eps) * weight + bias.
+
+    x [..., D] fp32 or bf16, weight [D] fp32, bias [D] fp32 or None.  Returns y
+    (x's dtype), or (y, mean [...], rstd [...] fp32) with ``want_stats``, which
+    layer_norm_backward needs."""
+    y, _, mean, rstd = _layer_norm(x, None, weight, bias, None, eps, y, None, want_stats)
+    return (y, mean, rstd) if want_stats else y
+
+
+def add_layer_norm(x, residual, weight, bias=None, *, scale=None, eps: float = 1e-5, y=None, residual_out=None,
+                   want_stats: bool = False):
+    """Residual addition and the layer norm in front of the next block:
+
+        residual_out = residual + scale * x,  y = layer_norm(residual_out)
+
+    as add_rms_norm: x [..., D] fp32 or bf16, residual of x's shape in x's dtype
+    or fp32, weight, bias (or None) and ``scale`` (or None) [D] fp32;
+    ``residual_out`` may be residual itself; the norm is that of the fp32 sum.
+    Returns (y, residual_out), or (y, residual_out, mean, rstd) with
+    ``want_stats``, which add_layer_norm_backward needs."""
+    if residual is None:
+        raise ValueError("residual is None: layer_norm takes x alone")
+    got = _layer_norm(x, residual, weight, bias, scale, eps, y, residual_out, want_stats)
+    return got if want_stats else got[:2]
+
+
+def _layer_norm_backward(dy, out, weight, mean, rstd, dresidual_out, x, scale, dx, dresidual, want_dbias, workspace):
+    index = _gpu(dy, out, weight, mean, rstd, dresidual_out, x, scale, dx, dresidual, workspace)
+    f32, shape, dtype, rdtype = _torch().float32, dy.shape, dy.dtype, out.dtype
+    if scale is not None and x is None:
+        raise ValueError("the gradient of scale needs x")
+    _need(dy, shape, dtype, "dy")
+    _need(out, shape, rdtype, "the normed input")
+    _need(weight, shape[-1:], f32, "weight")
+    _need(mean, shape[:-1], f32, "mean")
+    _need(rstd, shape[:-1], f32, "rstd")
+    _need(dresidual_out, shape, rdtype, "dresidual_out")
+    _need(x, shape, dtype, "x")
+    _need(scale, shape[-1:], f32, "scale")
+    _need(dx, shape, dtype, "dx")
+    _need(dresidual, shape, rdtype, "dresidual")
+    sh = _norm_shape(dy, dtype, rdtype, 0.0)
+    one = scale is None and rdtype == dtype and (dx is None or dresidual is None)
+    if one:
+        dx = dresidual = dx if dx is not None else dresidual if dresidual is not None else _new(dy, shape, dtype)
+    else:
+        dx = _new(dy, shape, dtype) if dx is None else dx
+        dresidual = _new(dy, shape, rdtype) if dresidual is None else dresidual
+    dweight = _new(weight, weight.shape, f32)
+    dbias = _new(weight, weight.shape, f32) if want_dbias else None
+    dscale = None if scale is None else _new(scale, scale.shape, f32)
+    workspace = _workspace(workspace, _layer_norm_bytes(sh.rows, sh.columns), dy)
+    _launch(index, "ssd_layer_norm_backward", dy.data_ptr(), _p(dresidual_out), out.data_ptr(), weight.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr(), None if scale is None else x.data_ptr(), _p(scale), dx.data_ptr(),
+            None if one else dresidual.data_ptr(), dweight.data_ptr(), _p(dbias), _p(dscale), ctypes.byref(sh),
+            workspace.data_ptr(), _bytes(workspace))
+    return dx, dresidual, dweight, dbias, dscale
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, want_dbias: bool = True, dx=None, workspace=None):
+    """Gradients of layer_norm for dy (x's dtype) from its x, mean and rstd:
+    (dx, dweight, dbias or None)."""
+    if x.dtype != dy.dtype:
+        raise TypeError("dy has dtype %s, expected %s" % (dy.dtype, x.dtype))
+    dx, _, dweight, dbias, _ = _layer_norm_backward(dy, x, weight, mean, rstd, None, None, None, dx, None, want_dbias,
+                                                    workspace)
+    return dx, dweight, dbias
+
+
+def add_layer_norm_backward(dy, residual_out, weight, mean, rstd, *, dresidual_out=None, x=None, scale=None, dx=None,
+                            dresidual=None, want_dbias: bool = True, workspace=None):
+    """Gradients of add_layer_norm for dy (x's dtype) and ``dresidual_out``
+    (residual's dtype; None: zero), from its residual_out, mean and rstd.  With
+    ``scale``, x is needed for its gradient.  Returns (dx, dresidual, dweight,
+    dbias or None, dscale or None); without a scale and with one dtype dx and
+    dresidual are the same tensor unless both are given."""
+    return _layer_norm_backward(dy, residual_out, weight, mean, rstd, dresidual_out, x, scale, dx, dresidual,
+                                want_dbias, workspace)
 
 
 def _gated_norm_shape(x, z, weight, groups, eps, norm_before_gate):

@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libssd_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["ssd_api.cpp", "ssd_prefill.hip", "ssd_scan_walk.hip", "ssd_decode.hip", "ssd_conv.hip",
-           "ssd_noalloc.hip", "ssd_block_api.cpp", "ssd_gated.hip", "ssd_norm.hip", "ssd_conv_bwd.hip",
+           "ssd_noalloc.hip", "ssd_block_api.cpp", "ssd_gated.hip", "ssd_norm.hip", "ssd_layer_norm.hip", "ssd_conv_bwd.hip",
            "ssd_selective_api.cpp", "ssd_selective.hip", "ssd_selective_bwd.hip"]
 ARCH = "gfx950"
 

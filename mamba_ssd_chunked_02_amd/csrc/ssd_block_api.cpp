@@ -426,3 +426,99 @@ SSD_API ssd_status ssd_gated_rms_norm_backward(const void* dy, const void* x, co
     a.part = (float*)workspace;
     return queued(ssd::launch_gated_norm_backward(a, (hipStream_t)stream));
 }
+
+// ------------------------------------------------------------------ layer norm
+namespace {
+
+// dweight's, dbias's and dscale's partial sums.
+size_t layer_norm_workspace(const ssd::NormArgs& a) { return (size_t)a.nparts * a.D * 12; }
+
+}  // namespace
+
+SSD_API ssd_status ssd_layer_norm(const void* x, const void* residual, const float* weight, const float* bias,
+                                  const float* scale, void* y, void* out, float* mean, float* rstd,
+                                  const ssd_norm_shape* shape, void* stream) {
+    ssd::NormArgs a;
+    ssd_status st = norm_shape_of(shape, false, &a);
+    if (st != SSD_OK) return st;
+    const bool any = a.rows > 0;
+    if (!residual && (scale || out) && any) FAIL(SSD_ERR_SHAPE, "%s without residual", scale ? "scale" : "out");
+    if (!residual && a.a_f32 != a.b_f32 && any) FAIL(SSD_ERR_DTYPE, "a second dtype without residual");
+    const Arg args[] = {{x, "x", any, false},           {residual, "residual", false, false},
+                        {weight, "weight", true, false}, {bias, "bias", false, false},
+                        {scale, "scale", false, false},  {y, "y", any, true},
+                        {out, "out", any && residual, true}, {mean, "mean", false, true},
+                        {rstd, "rstd", false, true}};
+    // a lane reads its elements of x and the residual before it writes out; x may be the residual
+    const bool in_place = out && out == residual;
+    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])),
+                    {in_place ? 6 : -1, 1u << 1 | (a.a_f32 == a.b_f32 ? 1u << 0 : 0)});
+    if (st != SSD_OK) return st;
+    a.x = x;
+    a.z = residual;
+    a.weight = weight;
+    a.bias = bias;
+    a.scale = scale;
+    a.y = y;
+    a.out = out;
+    a.mean = mean;
+    a.rstd = rstd;
+    return queued(ssd::launch_layer_norm(a, (hipStream_t)stream));
+}
+
+SSD_API ssd_status ssd_layer_norm_backward_workspace_size(const ssd_norm_shape* shape, size_t* bytes) {
+    if (!bytes) FAIL(SSD_ERR_NULL, "bytes is NULL");
+    ssd::NormArgs a;
+    const ssd_status st = norm_shape_of(shape, false, &a);
+    if (st != SSD_OK) return st;
+    *bytes = layer_norm_workspace(a);
+    return ok();
+}
+
+SSD_API ssd_status ssd_layer_norm_backward(const void* dy, const void* dout, const void* out, const float* weight,
+                                           const float* mean, const float* rstd, const void* x, const float* scale,
+                                           void* dx, void* dresidual, float* dweight, float* dbias, float* dscale,
+                                           const ssd_norm_shape* shape, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+    ssd::NormArgs a;
+    ssd_status st = norm_shape_of(shape, false, &a);
+    if (st != SSD_OK) return st;
+    const bool any = a.rows > 0;
+    if (!scale && dscale) FAIL(SSD_ERR_SHAPE, "dscale without scale");
+    const Arg args[] = {{dy, "dy", any, false},
+                        {dout, "dout", false, false},
+                        {out, "out", any, false},
+                        {weight, "weight", true, false},
+                        {mean, "mean", any, false},
+                        {rstd, "rstd", any, false},
+                        {x, "x", any && dscale, false},
+                        {scale, "scale", false, false},
+                        {dx, "dx", any, true},
+                        {dresidual, "dresidual", false, true},
+                        {dweight, "dweight", true, true},
+                        {dbias, "dbias", false, true},
+                        {dscale, "dscale", false, true}};
+    // a lane reads its elements of dout, and of dy, out and x where dout is one of them, before it writes the gradient
+    const bool one_type = a.a_f32 == a.b_f32;
+    const int in_place = !dout ? -1 : dresidual == dout ? 9 : dx == dout && one_type ? 8 : -1;
+    st = check_args(args, (int)(sizeof(args) / sizeof(args[0])),
+                    {in_place, 1u << 1 | 1u << 2 | (one_type ? 1u << 0 | 1u << 6 : 0)});
+    if (st != SSD_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, layer_norm_workspace(a));
+    if (st != SSD_OK) return st;
+    a.dy = dy;
+    a.dout = dout;
+    a.out = const_cast<void*>(out);  // read only here
+    a.weight = weight;
+    a.mean_in = mean;
+    a.rstd_in = rstd;
+    a.x = x;
+    a.scale = scale;
+    a.dx = dx;
+    a.dz = dresidual;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.dscale = dscale;
+    a.part = (float*)workspace;
+    return queued(ssd::launch_layer_norm_backward(a, (hipStream_t)stream));
+}

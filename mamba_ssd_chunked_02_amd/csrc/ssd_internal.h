@@ -314,7 +314,7 @@ hipError_t launch_selective_scan(const SelArgs& a, const SelLayout& lay, void* w
 hipError_t launch_selective_backward(const SelArgs& a, const SelLayout& lay, void* ws, hipStream_t stream);
 hipError_t launch_selective_step(const SelArgs& a, const float* state, float* state_out, hipStream_t stream);
 
-// RMS norms (ssd_norm.hip).  A segment is one row's part that shares a norm
+// Norms (ssd_norm.hip, ssd_layer_norm.hip).  A segment is one row's part that shares a norm
 // (the whole row, or one of its groups).
 struct NormArgs {
     int64_t rows;
@@ -325,18 +325,22 @@ struct NormArgs {
     const void* x;             // [rows, D]
     const void* z;             // residual norm: the residual; gated norm: the gate's input
     const float* weight;       // [D]
-    const float* scale;        // residual norm: [D] or NULL
+    const float* bias;         // layer norm: [D] or NULL
+    const float* scale;        // residual and layer norm: [D] or NULL
     int32_t norm_first;        // gated norm: the gate multiplies the normalised row
     void* y;                   // [rows, D]
     void* out;                 // residual norm: the new residual [rows, D]
     float* rstd;               // [rows, G] or NULL
+    float* mean;               // layer norm: [rows] or NULL
     // backward
     const void* dy;
     const void* dout;          // residual norm: gradient of the new residual, or NULL
     const float* rstd_in;
+    const float* mean_in;
     void* dx;
     void* dz;                  // residual norm: gradient of the residual
     float* dweight;            // [D]
+    float* dbias;              // layer norm: [D] or NULL
     float* dscale;             // [D] or NULL
     float* part;               // workspace
     int32_t nparts;            // workgroups along the rows, each with its own partial sums
@@ -348,6 +352,8 @@ constexpr int32_t kMaxNormColumns = 16384;
 int32_t norm_parts(int64_t rows, int32_t D, int32_t G);
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_residual_norm_backward(const NormArgs& a, hipStream_t stream);
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream);  // z, out: NULL without a residual
+hipError_t launch_layer_norm_backward(const NormArgs& a, hipStream_t stream);
 hipError_t launch_gated_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_gated_norm_backward(const NormArgs& a, hipStream_t stream);
 

@@ -1,0 +1,266 @@
+// Layer norm on gfx950, with the residual addition of the block before:
+//   u = residual + scale x   (or u = x),   y = (u - mean(u)) rstd w + b
+// with rstd = 1 / sqrt(mean((u - mean(u))^2) + eps) per row.
+// A few operations per element read: HBM streams.  A row is held in registers
+// between its sums and its use, so every input is read once.
+//
+// The mean is taken first and the squares of the distances from it then, both from
+// registers: a row whose mean is large against its spread keeps its digits.  The
+// first mean's own rounding shows in the sum of the distances, which comes with the
+// second sum, and is taken off again.
+#include <type_traits>
+
+#include "ssd_norm_rows.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int64_t kMaxBlocks = 1 << 22;  // a launch counts its lanes in 32 bits
+
+// ------------------------------------------------------------------ forward
+// A: type of x and y, B: of the residual (RES).
+template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
+__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void layer_norm_kernel(NormArgs a) {
+    __shared__ float lds[kMaxWaves], lds2[kMaxWaves][2];
+    constexpr bool SPLIT = sizeof(A) == 4 || (RES && sizeof(B) == 4);
+    typedef Eight<A, SPLIT> EA;
+    typedef Eight<B, SPLIT> EB;
+    typedef Eight<float, SPLIT> EW;
+    const Team<LANES, WIDE, V> p;
+    const int n = a.D;
+    // as many rounds as the workgroup's first team has: a team without a row
+    // still takes part in its wave's shuffles
+    const int64_t first = (int64_t)blockIdx.x * (WIDE ? 1 : (int)blockDim.x / LANES);
+    for (int64_t s0 = first, row = p.index; s0 < a.rows; s0 += p.teams, row += p.teams) {
+        const bool on = row < a.rows;
+        const int64_t at = on ? row * n : 0;
+        typename EA::raw ra[V];
+        typename EB::raw rb[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols k = p.template cols<SPLIT>(v, on ? n : 0);
+            ra[v] = EA::load((const A*)a.x + at, k);
+            if constexpr (RES) rb[v] = EB::load((const B*)a.z + at, k);
+        }
+        f32x8 u[V];
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols k = p.template cols<SPLIT>(v, on ? n : 0);
+            u[v] = EA::widen(ra[v]);
+            if constexpr (RES) {
+                const f32x8 r = EB::widen(rb[v]);
+                u[v] = a.scale ? r + EW::cached(a.scale, k) * u[v] : r + u[v];
+                EB::store((B*)a.out + at, k, u[v]);
+            }
+            sum += sum8(u[v]);
+        }
+        const float mean = p.sum(sum, lds) / (float)n;
+        float rest = 0.f, ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols k = p.template cols<SPLIT>(v, on ? n : 0);
+            u[v] = away_from(u[v], mean, k);
+            rest += sum8(u[v]);
+            ss += sum8(u[v] * u[v]);
+        }
+        p.sum2(rest, ss, lds2);
+        rest /= (float)n;
+        const float rstd = 1.f / sqrtf(fmaxf(ss / (float)n - rest * rest, 0.f) + a.eps);
+        if (!on) continue;
+        if (p.lane == 0) {
+            if (a.mean) a.mean[row] = mean + rest;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols k = p.template cols<SPLIT>(v, n);
+            f32x8 y = (u[v] - rest) * rstd * EW::cached(a.weight, k);
+            if (a.bias) y += EW::cached(a.bias, k);
+            EA::store((A*)a.y + at, k, y);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// With m = (u - mean) rstd and d the gradient of y:
+//   du = dout + rstd (w d - mean(w d) - m mean(w d m)),  dx = scale du,
+//   dw = sum over rows of d m,  db of d,  dscale of du x.
+// Team k takes the rows k, k + teams, ..., the next one's data in flight, and keeps
+// its sums over rows in registers; a workgroup's go to its own row of the partial
+// sums, which a second kernel adds.
+template <typename A, typename B, int LANES, bool WIDE, int V>
+__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void layer_norm_backward_kernel(NormArgs a) {
+    __shared__ float lds[kMaxWaves][2];
+    __shared__ f32x4 sums[WIDE ? 1 : 3 * 64 * V * 2];
+    constexpr bool SPLIT = sizeof(A) == 4 || sizeof(B) == 4;
+    typedef Eight<A, SPLIT> EA;
+    typedef Eight<B, SPLIT> EB;
+    typedef Eight<float, SPLIT> EW;
+    const Team<LANES, WIDE, V> p;
+    const int n = a.D;
+    const bool scaled = a.dscale;
+    struct Row {
+        typename EA::raw dy[V], x[V];
+        typename EB::raw u[V], dout[V];
+        float mean, rstd;
+    };
+    auto load = [&](int64_t row, Row& r) {
+        const bool there = row < a.rows;
+        r.mean = there ? a.mean_in[row] : 0.f;
+        r.rstd = there ? a.rstd_in[row] : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols k = p.template cols<SPLIT>(v, there ? n : 0);
+            r.dy[v] = EA::load((const A*)a.dy + row * n, k);
+            r.u[v] = EB::load((const B*)a.out + row * n, k);
+            r.dout[v] = {};
+            r.x[v] = {};
+            if (a.dout) r.dout[v] = EB::load((const B*)a.dout + row * n, k);
+            if (scaled) r.x[v] = EA::load((const A*)a.x + row * n, k);
+        }
+    };
+    f32x8 w[V], sc[V], acc[3][V] = {};  // dw, db, dscale
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const Cols k = p.template cols<SPLIT>(v, n);
+        w[v] = EW::cached(a.weight, k);
+        sc[v] = a.scale ? EW::cached(a.scale, k) : f32x8{1, 1, 1, 1, 1, 1, 1, 1};
+    }
+    constexpr bool kAhead = V < 4;  // there are no registers for the next row of the widest ones
+    Row cur, nxt;
+    if (kAhead) load(p.index, nxt);
+    // WIDE: the same rows for the whole workgroup; else as many rounds as the
+    // workgroup's first team has, so that a wave's teams stay together
+    const int64_t first = (int64_t)blockIdx.x * (WIDE ? 1 : (int)blockDim.x / LANES);
+    for (int64_t r0 = first, row = p.index; r0 < a.rows; r0 += p.teams, row += p.teams) {
+        if (kAhead) {
+            cur = nxt;
+            load(row + p.teams, nxt);
+        } else {
+            load(row, cur);
+        }
+        f32x8 m[V], wd[V];
+        float mean1 = 0.f, mean2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const f32x8 d = EA::widen(cur.dy[v]);
+            m[v] = (EB::widen(cur.u[v]) - cur.mean) * cur.rstd;
+            wd[v] = d * w[v];
+            acc[0][v] += d * m[v];
+            acc[1][v] += d;
+            mean1 += sum8(wd[v]);
+            mean2 += sum8(wd[v] * m[v]);
+        }
+        p.sum2(mean1, mean2, lds);
+        mean1 /= (float)n;
+        mean2 /= (float)n;
+        if (row >= a.rows) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Cols k = p.template cols<SPLIT>(v, n);
+            const f32x8 du = (wd[v] - mean1 - m[v] * mean2) * cur.rstd + EB::widen(cur.dout[v]);
+            if (a.dz) EB::store((B*)a.dz + row * n, k, du);
+            if (scaled) acc[2][v] += du * EA::widen(cur.x[v]);
+            EA::store((A*)a.dx + row * n, k, du * sc[v]);
+        }
+    }
+    // this workgroup's sums over its rows
+#pragma unroll
+    for (int o = 0; o < 3; ++o) {
+        if ((o == 1 && !a.dbias) || (o == 2 && !scaled)) continue;
+        f32x8(&s)[V] = acc[o];
+        float* to = a.part + ((int64_t)o * a.nparts + blockIdx.x) * n;
+        if constexpr (!WIDE) {
+            // the wave's teams hold the same columns; then waves 1..3 through LDS
+#pragma unroll
+            for (int d = LANES; d < 64; d <<= 1)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[v][e] += __shfl_xor(s[v][e], d);
+            const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+            __syncthreads();
+            if (wave) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    sums[(((wave - 1) * V + v) * 2) * 64 + lane] = __builtin_shufflevector(s[v], s[v], 0, 1, 2, 3);
+                    sums[(((wave - 1) * V + v) * 2 + 1) * 64 + lane] = __builtin_shufflevector(s[v], s[v], 4, 5, 6, 7);
+                }
+            }
+            __syncthreads();
+            if (wave || lane >= LANES) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const f32x4 lo = sums[((i * V + v) * 2) * 64 + lane], hi = sums[((i * V + v) * 2 + 1) * 64 + lane];
+                    s[v] += __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) EW::store_cached(to, p.template cols<SPLIT>(v, n), s[v]);
+    }
+}
+
+// dweight, dbias and dscale (blockIdx.y: which of those wanted) from the workgroups' partial sums.
+__global__ __launch_bounds__(kSumThreads) void layer_norm_sums_kernel(NormArgs a, int64_t n) {
+    float* const to[3] = {a.dweight, a.dbias, a.dscale};
+    const int o = blockIdx.y == 0 ? 0 : blockIdx.y == 1 && a.dbias ? 1 : 2;
+    const int col = blockIdx.x * kSumCols + threadIdx.x % kSumCols;
+    const float* part = a.part + (int64_t)o * a.nparts * a.D;
+    const float s = column_sum(n, [&](int64_t t) { return col < a.D ? part[t * a.D + col] : 0.f; });
+    if (threadIdx.x < kSumCols && col < a.D) to[o][col] = s;
+}
+
+template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
+hipError_t run_layer_norm(const NormArgs& a, bool backward, hipStream_t stream) {
+    const int threads = WIDE ? norm_threads(a.D, V) : 256;
+    if (backward) {
+        if (a.rows > 0) {
+            hipLaunchKernelGGL((layer_norm_backward_kernel<A, B, LANES, WIDE, V>), dim3(a.nparts), dim3(threads), 0, stream,
+                               a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL(layer_norm_sums_kernel,
+                           dim3((a.D + kSumCols - 1) / kSumCols, 1 + (a.dbias != nullptr) + (a.dscale != nullptr)),
+                           dim3(kSumThreads), 0, stream, a, (int64_t)(a.rows > 0 ? a.nparts : 0));
+        return hipGetLastError();
+    }
+    const int64_t per = WIDE ? 1 : 256 / LANES;
+    if (a.rows == 0) return hipSuccess;
+    const int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, kMaxBlocks);
+    hipLaunchKernelGGL((layer_norm_kernel<A, B, RES, LANES, WIDE, V>), dim3((unsigned)blocks), dim3(threads), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <typename A, typename B, bool RES>
+hipError_t by_columns(const NormArgs& a, bool backward, hipStream_t stream) {
+    const int n = a.D;
+    if (n <= 8 * kVec) return run_layer_norm<A, B, RES, 8, false, 1>(a, backward, stream);
+    if (n <= 16 * kVec) return run_layer_norm<A, B, RES, 16, false, 1>(a, backward, stream);
+    if (n <= 32 * kVec) return run_layer_norm<A, B, RES, 32, false, 1>(a, backward, stream);
+    if (n <= 64 * kVec) return run_layer_norm<A, B, RES, 64, false, 1>(a, backward, stream);
+    switch (norm_vectors(n)) {
+        case 1: return run_layer_norm<A, B, RES, 64, true, 1>(a, backward, stream);
+        case 2: return run_layer_norm<A, B, RES, 64, true, 2>(a, backward, stream);
+        default: return run_layer_norm<A, B, RES, 64, true, 4>(a, backward, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
+    if (!a.z) return a.a_f32 ? by_columns<float, float, false>(a, false, stream) : by_columns<bf16_t, bf16_t, false>(a, false, stream);
+    if (a.a_f32) return by_columns<float, float, true>(a, false, stream);
+    return a.b_f32 ? by_columns<bf16_t, float, true>(a, false, stream) : by_columns<bf16_t, bf16_t, true>(a, false, stream);
+}
+
+hipError_t launch_layer_norm_backward(const NormArgs& a, hipStream_t stream) {
+    if (a.a_f32) return by_columns<float, float, true>(a, true, stream);
+    return a.b_f32 ? by_columns<bf16_t, float, true>(a, true, stream) : by_columns<bf16_t, bf16_t, true>(a, true, stream);
+}
+
+}  // namespace ssd

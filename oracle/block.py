@@ -127,6 +127,39 @@ def add_rms_norm_backward(dy, out, weight, rstd, dout=None, x=None, scale=None):
     return grads, scales
 
 
+def layer_norm(x, weight, bias=None, residual=None, scale=None, eps=1e-5):
+    """y, the normed input u, mean, rstd."""
+    u = f64(x) if scale is None else f64(scale) * f64(x)
+    if residual is not None:
+        u = u + f64(residual)
+    mean = np.mean(u, axis=-1)
+    d = u - mean[..., None]
+    rstd = 1.0 / np.sqrt(np.mean(d * d, axis=-1) + eps)
+    y = d * rstd[..., None] * f64(weight)
+    return (y if bias is None else y + f64(bias)), u, mean, rstd
+
+
+def layer_norm_backward(dy, out, weight, mean, rstd, dout=None, x=None, scale=None):
+    dy, w, mean, rstd = f64(dy), f64(weight), f64(mean)[..., None], f64(rstd)[..., None]
+    m = (f64(out) - mean) * rstd
+    ms = (np.abs(f64(out)) + np.abs(mean)) * rstd  # what the difference is taken of
+    wd = dy * w
+    c1, c2 = np.mean(wd, axis=-1, keepdims=True), np.mean(wd * m, axis=-1, keepdims=True)
+    c1s, c2s = np.mean(np.abs(wd), axis=-1, keepdims=True), np.mean(np.abs(wd) * ms, axis=-1, keepdims=True)
+    extra = np.zeros_like(m) if dout is None else f64(dout)
+    dres = extra + rstd * (wd - c1 - m * c2)
+    dres_s = np.abs(extra) + rstd * (np.abs(wd) + c1s + ms * np.abs(c2) + np.abs(m) * c2s)
+    s = 1.0 if scale is None else f64(scale)
+    axes = tuple(range(m.ndim - 1))
+    grads = dict(dx=dres * s, dresidual=dres, dweight=(dy * m).sum(axes), dbias=dy.sum(axes))
+    scales = dict(dx=dres_s * np.abs(s), dresidual=dres_s, dweight=(np.abs(dy) * ms).sum(axes),
+                  dbias=np.abs(dy).sum(axes))
+    if scale is not None:
+        grads["dscale"] = (dres * f64(x)).sum(axes)
+        scales["dscale"] = (dres_s * np.abs(f64(x))).sum(axes)
+    return grads, scales
+
+
 def gated_rms_norm(x, z, weight, groups=1, eps=1e-5, norm_first=False):
     x, z, w = f64(x), f64(z), f64(weight)
     v = x if norm_first else x * silu(z)
