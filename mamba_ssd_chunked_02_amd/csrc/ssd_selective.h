@@ -15,39 +15,72 @@
 
 namespace ssd {
 
-constexpr int kSelChannels = 16;       // of a wave
-constexpr int kSelBackChannels = 128;  // of a workgroup of the backward pass
+constexpr int kSelChannels = 16;  // of a wave
+constexpr int kSelBackWaves = 4;  // of a workgroup of the backward pass
+constexpr int kSelBackChannels = kSelBackWaves * kSelChannels;
 constexpr float kLog2e = 1.44269504088896341f;
 
 // Tokens of a tile, whose B and C are NB registers each.
-template <int NS>
+template <int STATES>
 struct SelTile {
-    static constexpr int TT = NS <= 4 ? 16 : 64 / NS;
+    static constexpr int NS = STATES;
+    static constexpr int TT = NS == 1 ? 16 : NS <= 8 ? 8 : 4;
     static constexpr int NB = TT * NS / 16;
     static constexpr int Q = TT / 4;  // tokens of a lane
 };
 
+// The same for the backward pass, which holds a tile's states and decays in
+// registers; SUB tokens lie between two states kept in LDS.
+template <int STATES>
+struct SelBack {
+    static constexpr int NS = STATES;
+    static constexpr int TT = NS == 1 ? 16 : NS <= 4 ? 8 : 4;
+    static constexpr int NB = TT * NS / 16;
+    static constexpr int Q = TT / 4;
+    static constexpr int SUB = NS <= 4 ? TT : 16;
+};
+
+// f(integral_constant<int, 0>) ... <N - 1>
+template <int N, int I = 0, typename F>
+__device__ inline void unroll(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<N, I + 1>(f);
+    }
+}
+
 // ---------------------------------------------------------------- elements
+// One element as it is loaded from a buffer, 0 where the offset lies behind its end.
+constexpr int kSelBufferWord3 = 0x00020000;            // gfx9 untyped data
+constexpr uint32_t kSelNowhere = 0x80000000u;          // behind the end of any of the buffers here
 template <typename T>
 struct One;
 template <>
 struct One<float> {
     typedef float raw;
     __device__ static inline raw load(const float* p) { return *p; }
+    __device__ static inline raw load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+        const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+        return __builtin_bit_cast(float, v);
+    }
+    __device__ static inline void store(__amdgpu_buffer_rsrc_t r, uint32_t at, float v) {
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, at, 0, 0);
+    }
     __device__ static inline float widen(raw v) { return v; }
 };
 template <>
 struct One<bf16_t> {
     typedef uint32_t raw;
     __device__ static inline raw load(const bf16_t* p) { return *(const uint16_t*)p; }
+    __device__ static inline raw load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+        return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+    }
+    __device__ static inline void store(__amdgpu_buffer_rsrc_t r, uint32_t at, float v) {
+        const bf16_t n = (bf16_t)v;
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, n), r, at, 0, 0);
+    }
     __device__ static inline float widen(raw v) { return __builtin_bit_cast(float, v << 16); }
 };
-
-// One element of y or of a gradient in either type.
-__device__ inline void store_one(void* p, int64_t at, bool f32, float v) {
-    if (f32) ((float*)p)[at] = v;
-    else ((bf16_t*)p)[at] = (bf16_t)v;
-}
 
 // ---------------------------------------------------------------- rows
 // The halves of a and b: a = [a.lo, b.lo], b = [a.hi, b.hi].
@@ -101,27 +134,164 @@ __device__ inline float row_lane(float v) {
                               __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x150 + I, 0xf, 0xf, true));
 }
 
-// f(integral_constant<int, 0>) ... <N - 1>
-template <int N, int I = 0, typename F>
-__device__ inline void unroll(F&& f) {
-    if constexpr (I < N) {
-        f(std::integral_constant<int, I>{});
-        unroll<N, I + 1>(f);
+// What the wave wrote to LDS before this is read after it: LDS works for a wave in
+// order, the compiler has to as well.
+__device__ inline void in_wave_order() {
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// acc += src[lane F + j of its row] v[j] for j = 0..3: the multiplication takes its
+// operand across the row, which the compiler does only for plain products (with a
+// move otherwise: 7 cycles in place of 4.6).  The operand must not have been written
+// in the two instructions before.
+template <int F>
+__device__ inline void dot_row4(float& acc, float src, float v0, float v1, float v2, float v3) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "+v"(acc)
+        : "v"(src), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
+}
+// acc_j += src[lane F + j of its row] v.
+template <int F>
+__device__ inline void add_row4(float& a0, float& a1, float& a2, float& a3, float src, float v) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %4, %5 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %5 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %5 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "+v"(a0), "+v"(a1), "+v"(a2), "+v"(a3)
+        : "v"(src), "v"(v), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
+}
+// The same for the NS states of a token, whose first one is at lane F.
+template <int F, int NS>
+__device__ inline void dot_row(float& acc, float src, const float (&v)[NS]) {
+    if constexpr (NS >= 4) {
+        unroll<NS / 4>([&](auto four) {
+            constexpr int o = 4 * decltype(four)::value;
+            dot_row4<F + o>(acc, src, v[o], v[o + 1], v[o + 2], v[o + 3]);
+        });
+    } else {
+        unroll<NS>([&](auto one) {
+            constexpr int j = decltype(one)::value;
+            acc = __builtin_fmaf(row_lane<F + j>(src), v[j], acc);
+        });
+    }
+}
+template <int F, int NS>
+__device__ inline void add_row(float (&acc)[NS], float src, float v) {
+    if constexpr (NS >= 4) {
+        unroll<NS / 4>([&](auto four) {
+            constexpr int o = 4 * decltype(four)::value;
+            add_row4<F + o>(acc[o], acc[o + 1], acc[o + 2], acc[o + 3], src, v);
+        });
+    } else {
+        unroll<NS>([&](auto one) {
+            constexpr int j = decltype(one)::value;
+            acc[j] = __builtin_fmaf(row_lane<F + j>(src), v, acc[j]);
+        });
     }
 }
 
+// ---------------------------------------------------------------- rows in memory
+// The compiler shall keep one scalar pointer a tensor, not one for every load of a
+// tile (which runs out of scalar registers and then adds in vector ones).
+__device__ inline const char* opaque(const char* p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
+// A tensor's rows of a tile as a buffer that ends with the last row that is there:
+// rows behind it read as 0 and are not written.
+struct TileRows {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t lane, stride;
+    // row: a constant
+    __device__ inline uint32_t at(int row) const { return lane + row * stride; }
+};
+// A tensor of rows as a wave reads it, from the first row of a tile of TT: lane
+// 16 q + k takes row 4 i + q of its channel.
+template <int TT>
+struct RowsOf {
+    const char* p;
+    uint32_t stride, width, lane;  // bytes
+    __device__ inline RowsOf(const void* base, int64_t row, int64_t elements, int size, int C, int c, int q)
+        : p((const char*)base + row * elements * size), stride((uint32_t)elements * size), width((uint32_t)C * size),
+          lane(q * stride + c * size) {}
+    __device__ inline void move(int rows) { p = opaque(p + rows * (int64_t)stride); }
+    __device__ inline TileRows tile(int left) const {
+        const uint32_t bytes = (min(left, TT) - 1) * stride + width;
+        return {__builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, (int)bytes, kSelBufferWord3), lane,
+                stride};
+    }
+};
+// B or C of a tile of geometry G: register i holds state f % NS of the row's quarter
+// for token f / NS, f = 16 i + k; 0 for states behind the last one.
+template <typename T, typename G>
+struct StatesOf {
+    static constexpr int NS = G::NS, P = 16 / NS;  // tokens of a register
+    const char* p;
+    uint32_t stride, width, lane;
+    __device__ inline StatesOf(const void* base, int64_t row, int64_t elements, int first, int N, int q, int k)
+        : p((const char*)base + (row * elements + first) * (int64_t)sizeof(T)), stride((uint32_t)elements * sizeof(T)),
+          width(N * sizeof(T)) {
+        const int s = q * NS + k % NS;
+        lane = s < N ? k / NS * stride + s * (uint32_t)sizeof(T) : kSelNowhere;
+    }
+    __device__ inline void move(int rows) { p = opaque(p + rows * (int64_t)stride); }
+    __device__ inline void load(int left, typename One<T>::raw (&to)[G::NB]) const {
+        const uint32_t bytes = (min(left, G::TT) - 1) * stride + width;
+        const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, (int)bytes, kSelBufferWord3);
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i) to[i] = One<T>::load(r, lane + i * P * stride);
+    }
+    __device__ static inline void widen(const typename One<T>::raw (&r)[G::NB], float (&to)[G::NB]) {
+#pragma unroll
+        for (int i = 0; i < G::NB; ++i) to[i] = One<T>::widen(r[i]);
+    }
+};
+// y and dy may be of the other type than x.
+__device__ inline uint32_t load_either(const TileRows& r, int row, bool f32) {
+    return f32 ? __builtin_amdgcn_raw_buffer_load_b32(r.r, r.at(row), 0, 0)
+               : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r.r, r.at(row), 0, 0);
+}
+__device__ inline float widen_either(uint32_t v, bool f32) {
+    const uint32_t bits = f32 ? v : v << 16;
+    return __builtin_bit_cast(float, bits);
+}
+
 // ---------------------------------------------------------------- step sizes
+// log2(e) A, the factor of the step size in a decay's exponent.  Kept finite below, so
+// that a step of 0 leaves the state as it is whatever A is: a tile's rows behind the
+// last token take such steps.  NaN stays NaN.
+__device__ inline float decay_rate(float A) { return __builtin_elementwise_maximum(A * kLog2e, -3.4028234e38f); }
+
+// softplus(v) = max(v, 0) + log(1 + u), u = exp(-|v|): 13 operations, off by 2.4 of
+// 2^-24 for v >= 0, 7 for v > -15, 9 for v > -30 (measured on 2^22 values).  The
+// exponent's product is taken in two parts; what 1 + u loses of u is added again.
+// NaN stays NaN; exp(v) too small for a normal number counts as 0.
+__device__ inline float softplus_quick(float v) {
+    const float n = __builtin_elementwise_maximum(-fabsf(v), -88.f), t = n * 0x1.715476p+0f;
+    const float lo = __builtin_fmaf(n, 0x1.715476p+0f, -t), u0 = __builtin_amdgcn_exp2f(t);
+    const float u = __builtin_fmaf(u0 * 0x1.62e43p-1f, lo, u0), w = 1.f + u;
+    return __builtin_elementwise_maximum(v, 0.f) +
+           __builtin_fmaf(__builtin_amdgcn_logf(w), 0x1.62e43p-1f, u - (w - 1.f));
+}
+
 // The step size from its raw value, bias and clamp; NaN stays NaN.
 struct StepSize {
     bool on, cut;
     float bias, lo, hi;
+    StepSize() = default;
     __device__ inline StepSize(const DtAct& a, int c) : on(a.on != 0), lo(a.lo), hi(a.hi) {
         cut = on && !(lo == 0.f && hi == __builtin_inff());
         bias = on && a.bias ? a.bias[c] : 0.f;
     }
     __device__ inline float operator()(float raw) const {
         if (!on) return raw;
-        float v = softplus_f(raw + bias);
+        float v = softplus_quick(raw + bias);
         if (cut) v = v < lo ? lo : v > hi ? hi : v;
         return v;
     }
@@ -132,5 +302,47 @@ struct StepSize {
         return cut && (step <= lo || step >= hi) ? 0.f : s;
     }
 };
+
+// ---------------------------------------------------------------- items
+__device__ inline int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+// An item is the same for all lanes: in scalar registers.
+__device__ inline SelItem uniform_item(SelItem e) {
+    e.seq = uniform64(e.seq);
+    e.lo = uniform64(e.lo);
+    e.n = uniform64(e.n);
+    e.first = uniform64(e.first);
+    e.index = uniform64(e.index);
+    e.last = __builtin_amdgcn_readfirstlane(e.last);
+    return e;
+}
+
+// ---------------------------------------------------------------- carry
+// Along the items of a sequence, in place: what an item ends with from zero becomes
+// what it ends with, h that in front of the first one.  p and steps: the first item's,
+// dp and ds from one item to the next.  Items' values are read some ahead of the
+// chain, whose latency this is.
+__device__ inline void carry(float* p, int64_t dp, const float* steps, int64_t ds, int64_t items, float A, float h) {
+    constexpr int AHEAD = 16;
+    for (int64_t i = 0; i < items; i += AHEAD, p += AHEAD * dp, steps += AHEAD * ds) {
+        const int n = (int)min(items - i, (int64_t)AHEAD);
+        float v[AHEAD], a[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int o = min(j, n - 1);
+            v[j] = p[o * dp];
+            a[j] = steps[o * ds];
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (j >= n) break;
+            h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * a[j]), h, v[j]);
+            p[j * dp] = h;
+        }
+    }
+}
 
 }  // namespace ssd

@@ -28,9 +28,11 @@ struct RawTile {
 
 // LOCAL: the states that items end with, from zero.  Else y, final and saved states.
 template <typename T, int NS, bool LOCAL>
-__global__ __launch_bounds__(64 * kWaves) void selective_kernel(SelArgs a, SelLayout lay, float* ends, float* steps) {
+__global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel(SelArgs a, SelLayout lay, float* ends, float* steps) {
     typedef SelTile<NS> G;
     constexpr int TT = G::TT, NB = G::NB, Q = G::Q;
+    // what the rows of a wave hand to each other: step sizes, and they times x
+    __shared__ float s_x[kWaves][TT][16][2];
     const int lane = threadIdx.x & 63, q = lane >> 4, k = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = a.C / a.G, nblk = (per + kBlockChannels - 1) / kBlockChannels * a.G;
@@ -38,7 +40,7 @@ __global__ __launch_bounds__(64 * kWaves) void selective_kernel(SelArgs a, SelLa
     for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
         const int64_t place = w / nblk;
         const int cb = (int)(w - place * nblk), g = cb / (nblk / a.G);
-        const SelItem e = sel_item(a.cu, a.nseq, a.L, a.T, lay.item, place);
+        const SelItem e = uniform_item(sel_item(a.cu, a.nseq, a.L, a.T, lay.item, place));
         if (e.seq < 0 || (LOCAL && e.last)) continue;
         const int c0 = g * per + (cb - g * (nblk / a.G)) * kBlockChannels + wave * kSelChannels, end = (g + 1) * per;
         if (c0 >= end) continue;
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(64 * kWaves) void selective_kernel(SelArgs a, SelLa
         for (int j = 0; j < NS; ++j) {
             const int s = q * NS + j;
             const bool there = s < a.N;
-            A[j] = there ? a.A[chan + s] * kLog2e : 0.f;
+            A[j] = there ? decay_rate(a.A[chan + s]) : 0.f;
             h[j] = 0.f;
             if (LOCAL) continue;
             if (e.index > 0) h[j] = ends[((place - 1) * a.C + c) * (4 * NS) + s];
@@ -62,74 +64,83 @@ __global__ __launch_bounds__(64 * kWaves) void selective_kernel(SelArgs a, SelLa
         const float D = !LOCAL && a.D ? a.D[c] : 0.f;
         float total = 0.f;
 
-        const T* xp = (const T*)a.x + e.lo * a.x_stride + c;
-        const T* dp = (const T*)a.dt + e.lo * a.dt_stride + c;
-        const T* zp = (const T*)a.z + e.lo * a.z_stride + c;
-        const T* bp = (const T*)a.B + e.lo * a.b_stride + g * a.N;
-        const T* cp = (const T*)a.Cm + e.lo * a.c_stride + g * a.N;
         const bool gated = !LOCAL && a.z;
-        auto load = [&](int t0, RawTile<T, NS>& r) {
+        typedef RowsOf<TT> Rows;
+        const int size = (int)sizeof(T), ysize = a.y_f32 ? 4 : 2;
+        Rows xs(a.x, e.lo, a.x_stride, size, a.C, c, q), dts(a.dt, e.lo, a.dt_stride, size, a.C, c, q);
+        Rows zs(a.z, e.lo, a.z_stride, size, a.C, c, q), ys(a.y, e.lo, a.C, ysize, a.C, c, q);
+        if (!on) ys.lane = kSelNowhere;
+        StatesOf<T, G> bs(a.B, e.lo, a.b_stride, g * a.N, a.N, q, k), cs(a.Cm, e.lo, a.c_stride, g * a.N, a.N, q, k);
+        // the next tile, of which `left` tokens are there
+        auto load = [&](int left, RawTile<T, NS>& r) {
+            const TileRows tx = xs.tile(left), td = dts.tile(left);
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
-                const int64_t t = min(t0 + 4 * i + q, n - 1);
-                r.x[i] = One<T>::load(xp + t * a.x_stride);
-                r.dt[i] = One<T>::load(dp + t * a.dt_stride);
-                if (gated) r.z[i] = One<T>::load(zp + t * a.z_stride);
+                r.x[i] = One<T>::load(tx.r, tx.at(4 * i));
+                r.dt[i] = One<T>::load(td.r, td.at(4 * i));
             }
+            bs.load(left, r.b);
+            xs.move(TT);
+            dts.move(TT);
+            bs.move(TT);
+            if constexpr (LOCAL) return;
+            cs.load(left, r.c);
+            cs.move(TT);
+            if (!gated) return;
+            const TileRows tz = zs.tile(left);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int f = 16 * i + k, s = min(q * NS + f % NS, a.N - 1);
-                const int64_t t = min(t0 + f / NS, n - 1);
-                r.b[i] = One<T>::load(bp + t * a.b_stride + s);
-                if (!LOCAL) r.c[i] = One<T>::load(cp + t * a.c_stride + s);
-            }
+            for (int i = 0; i < Q; ++i) r.z[i] = One<T>::load(tz.r, tz.at(4 * i));
+            zs.move(TT);
         };
-        // TAIL: only some of the tile's tokens are there
-        auto tile = [&](int t0, const RawTile<T, NS>& r, auto tail) {
-            constexpr bool TAIL = decltype(tail)::value;
+        // the tile's first `left` tokens; a row behind them takes a step of 0
+        auto tile = [&](int left, const RawTile<T, NS>& r) {
             float b[NB], cc[NB];
+            bs.widen(r.b, b);
+            if (!LOCAL) cs.widen(r.c, cc);
+            const TileRows ty = ys.tile(left);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int f = 16 * i + k;
-                const bool there = q * NS + f % NS < a.N && (!TAIL || t0 + f / NS < n);
-                b[i] = there ? One<T>::widen(r.b[i]) : 0.f;
-                cc[i] = !LOCAL && there ? One<T>::widen(r.c[i]) : 0.f;
+            for (int i = 0; i < Q; ++i) {
+                float dt = step(One<T>::widen(r.dt[i]));
+                if (left < TT) dt = 4 * i + q < left ? dt : 0.f;
+                if (LOCAL) total += dt;
+                *(f32x2*)s_x[wave][4 * i + q][k] = f32x2{dt, dt * One<T>::widen(r.x[i])};
             }
+            in_wave_order();
+            f32x2 next = *(const f32x2*)s_x[wave][0][k];
             unroll<Q>([&](auto group) {
                 constexpr int i = decltype(group)::value;
-                if (TAIL && t0 + 4 * i >= n) return;
-                const bool there = !TAIL || t0 + 4 * i + q < n;
-                const float x = One<T>::widen(r.x[i]), dt = there ? step(One<T>::widen(r.dt[i])) : 0.f;
-                if (LOCAL) total += dt;
-                float dts[4], xs[4], y[4];
-                rows_to_all(dt, dts);
-                rows_to_all(there ? dt * x : 0.f, xs);
+                float y[4];
                 unroll<4>([&](auto token) {
-                    constexpr int t = decltype(token)::value;
-                    const bool live = !TAIL || t0 + 4 * i + t < n;
-                    y[t] = 0.f;
+                    constexpr int t = decltype(token)::value, at = 4 * i + t;
+                    const f32x2 now = next;  // read one token ahead
+                    if (at + 1 < TT) next = *(const f32x2*)s_x[wave][at + 1 < TT ? at + 1 : 0][k];
                     unroll<NS>([&](auto state) {
-                        constexpr int j = decltype(state)::value, f = (4 * i + t) * NS + j;
-                        const float d = __builtin_amdgcn_exp2f(dts[t] * A[j]);
-                        h[j] = __builtin_fmaf(live ? d : 1.f, h[j], row_lane<f % 16>(b[f / 16]) * xs[t]);
-                        if (!LOCAL) y[t] = __builtin_fmaf(row_lane<f % 16>(cc[f / 16]), h[j], y[t]);
+                        constexpr int j = decltype(state)::value, f = at * NS + j;
+                        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(now[0] * A[j]), h[j],
+                                              row_lane<f % 16>(b[f / 16]) * now[1]);
                     });
+                    y[t] = 0.f;
+                    if constexpr (!LOCAL) dot_row<at * NS % 16>(y[t], cc[at * NS / 16], h);
                 });
                 if constexpr (!LOCAL) {
-                    float v = sum_rows(y) + D * x;
+                    float v = sum_rows(y) + D * One<T>::widen(r.x[i]);
                     if (gated) {
                         const float z = One<T>::widen(r.z[i]);
                         v *= z * sigmoid_f(z);
                     }
-                    if (on && there) store_one(a.y, (e.lo + t0 + 4 * i + q) * a.C + c, a.y_f32, v);
+                    if (a.y_f32) One<float>::store(ty.r, ty.at(4 * i), v);
+                    else One<bf16_t>::store(ty.r, ty.at(4 * i), v);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             });
+            in_wave_order();
+            if (!LOCAL) ys.move(TT);
         };
         RawTile<T, NS> cur, nxt;
-        if (n > 0) load(0, nxt);
+        if (n > 0) load(n, nxt);
         for (int t0 = 0; t0 < n; t0 += TT) {
             cur = nxt;
-            if (t0 + TT < n) load(t0 + TT, nxt);
+            if (t0 + TT < n) load(n - t0 - TT, nxt);
             if (!LOCAL && a.states_out && t0 % kSelStateRows == 0 && on) {
                 const int64_t at = sel_place(a.cu != nullptr, e.seq, e.first, a.L, kSelStateRows) +
                                    (e.index * lay.item + t0) / kSelStateRows;
@@ -137,8 +148,7 @@ __global__ __launch_bounds__(64 * kWaves) void selective_kernel(SelArgs a, SelLa
                 for (int j = 0; j < NS; ++j)
                     if (q * NS + j < a.N) a.states_out[at * a.C * a.N + chan + q * NS + j] = h[j];
             }
-            if (t0 + TT <= n) tile(t0, cur, std::false_type{});
-            else tile(t0, cur, std::true_type{});
+            tile(n - t0, cur);
         }
         if constexpr (LOCAL) {
             total = sum_all_rows(total);
@@ -168,15 +178,10 @@ __global__ __launch_bounds__(256) void selective_carry_kernel(SelArgs a, SelLayo
         if (items < 2) continue;
         const int c = (int)(at / padded), n = (int)(at - (int64_t)c * padded);
         const bool there = n < a.N;
-        const float A = there ? a.A[(int64_t)c * a.N + n] * kLog2e : 0.f;
-        float h = a.init && there ? a.init[(s * a.C + c) * a.N + n] : 0.f;
+        const float A = there ? decay_rate(a.A[(int64_t)c * a.N + n]) : 0.f;
+        const float h = a.init && there ? a.init[(s * a.C + c) * a.N + n] : 0.f;
         const int64_t place = sel_place(a.cu != nullptr, s, r.lo, a.L, lay.item);
-        float* p = ends + place * row + at;
-        const float* st = steps + place * a.C + c;
-        for (int64_t j = 0; j < items - 1; ++j, p += row, st += a.C) {
-            h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * *st), h, *p);
-            *p = h;
-        }
+        carry(ends + place * row + at, row, steps + place * a.C + c, a.C, items - 1, A, h);
     }
 }
 
@@ -202,7 +207,7 @@ __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, const fl
                 f32x4 h = *(const f32x4*)(state + i * a.N + n);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * (Ap[n + j] * kLog2e)), h[j],
+                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * decay_rate(Ap[n + j])), h[j],
                                           One<T>::widen(One<T>::load(bp + n + j)) * xs);
                     y = __builtin_fmaf(One<T>::widen(One<T>::load(cp + n + j)), h[j], y);
                 }
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, const fl
             }
         } else {
             for (int n = q; n < a.N; n += 4) {
-                const float h = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * (Ap[n] * kLog2e)), state[i * a.N + n],
+                const float h = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * decay_rate(Ap[n])), state[i * a.N + n],
                                                One<T>::widen(One<T>::load(bp + n)) * xs);
                 y = __builtin_fmaf(One<T>::widen(One<T>::load(cp + n)), h, y);
                 state_out[i * a.N + n] = h;
@@ -223,7 +228,10 @@ __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, const fl
             const float z = One<T>::widen(One<T>::load((const T*)a.z + s * a.z_stride + c));
             y *= z * sigmoid_f(z);
         }
-        if (q == 0) store_one(a.y, i, a.y_f32, y);
+        if (q == 0) {
+            if (a.y_f32) ((float*)a.y)[i] = y;
+            else ((bf16_t*)a.y)[i] = (bf16_t)y;
+        }
     }
 }
 
@@ -281,11 +289,17 @@ int64_t sel_saved_states(bool packed, int64_t nseq, int64_t L, int64_t T) {
 
 SelLayout sel_layout(const SelArgs& a, bool backward) {
     SelLayout l = {};
-    const int64_t waves = (a.C + kSelChannels - 1) / kSelChannels, target = 4096;
+    const int64_t waves = (a.C + kSelChannels - 1) / kSelChannels;
     const int padded = a.N <= 4 ? 4 : a.N <= 8 ? 8 : a.N <= 16 ? 16 : a.N <= 32 ? 32 : 64;
     auto up = [](int64_t v) { return std::max<int64_t>((v + kSelStateRows - 1) / kSelStateRows, 1) * kSelStateRows; };
-    if (!a.cu && a.nseq * waves >= target / 2) l.item = up(a.L);
-    else l.item = up((int64_t)((double)a.T * waves / target));
+    // Forward: sequences of one length that bring 2 waves a SIMD go as a whole (8 x 2048 x
+    // 5120: 569 us; cut 650), else items for 16 waves a SIMD, so that their unequal ends
+    // even out (packed 49152 x 8192: 1024 tokens 3.03 ms, 512 and 2048 3.05, 6144 3.6),
+    // but 128 tokens at least (4096 x 1536: 64 tokens 88 us, 128 80, 256 107).  Backward:
+    // always items, since no sequence count that is common fills two waves a SIMD evenly.
+    const int64_t least = backward ? 64 : 128;
+    if (!backward && !a.cu && a.nseq * waves >= 2048) l.item = up(a.L);
+    else l.item = std::max(least, up((int64_t)((double)a.T * waves / 16384)));
     l.places = sel_places(a.cu != nullptr, a.nseq, a.L, a.T, l.item);
     l.whole = !a.cu ? l.item >= a.L : l.item >= a.T;
     size_t at = 0;

@@ -20,62 +20,82 @@ namespace ssd {
 
 namespace {
 
-constexpr int kWaves = kSelBackChannels / kSelChannels;  // of a workgroup
-constexpr int kSub = 16;   // tokens between two states in LDS
-constexpr int kSubs = (int)kSelStateRows / kSub;
+constexpr int kWaves = kSelBackWaves;  // of a workgroup
 constexpr int64_t kMaxBlocks = 1 << 22;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // ---------------------------------------------------------------- sums over channels
-// Lane k of a row: the sum of v[k] over the row's 16 lanes.  Every step sends half
-// of what a lane holds to the lane opposite.
+// Which half of its 16, 8, 4 and 2 lanes a lane is in, as masks: a select by one
+// takes half of what one by a condition code takes.
+struct Halves {
+    uint32_t m[4];
+    __device__ inline Halves(int k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = k >> i & 1 ? 0xffffffffu : 0u;
+            asm volatile("" : "+v"(m[i]));  // or the compiler makes conditions of them again
+        }
+    }
+};
 template <int CTRL>
 __device__ inline float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-__device__ inline float sum_channels(const float (&v)[16], int k) {
-    float a[8], b[4], c[2];
-    const bool b3 = k & 8, b2 = k & 4, b1 = k & 2, b0 = k & 1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = (b3 ? v[i + 8] : v[i]) + dpp<0x140>(b3 ? v[i] : v[i + 8]);  // row_mirror
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = (b2 ? a[i + 4] : a[i]) + dpp<0x141>(b2 ? a[i] : a[i + 4]);  // row_half_mirror
-#pragma unroll
-    for (int i = 0; i < 2; ++i) c[i] = (b1 ? b[i + 2] : b[i]) + dpp<0x1b>(b1 ? b[i] : b[i + 2]);   // quad_perm:[3,2,1,0]
-    return (b0 ? c[1] : c[0]) + dpp<0xb1>(b0 ? c[0] : c[1]);                                       // quad_perm:[1,0,3,2]
+__device__ inline float pick(uint32_t m, float set, float clear) {
+    const uint32_t s = __builtin_bit_cast(uint32_t, set), c = __builtin_bit_cast(uint32_t, clear), r = (m & s) | (~m & c);
+    return __builtin_bit_cast(float, r);
 }
-
-template <typename T, int NS>
-__device__ inline void load_states_of(const T* p, int64_t stride, int t0, int n, int N, int q, int k,
-                                      typename One<T>::raw (&to)[SelTile<NS>::NB]) {
+// a and b, each summed over twice as many lanes, in one: a lane keeps the value of
+// its half and takes it from the lane opposite.
+template <int STEP>
+__device__ inline float halve(float a, float b, const Halves& h) {
+    // row_mirror, row_half_mirror, quad_perm:[3,2,1,0], quad_perm:[1,0,3,2]
+    constexpr int CTRL = STEP == 0 ? 0x140 : STEP == 1 ? 0x141 : STEP == 2 ? 0x1b : 0xb1;
+    const uint32_t m = h.m[3 - STEP];
+    return pick(m, b, a) + dpp<CTRL>(pick(m, a, b));
+}
+// Sums over the 16 channels of a row of 16 values, NS states of P = 16 / NS tokens,
+// taken as they come: lane P j + t of the row gets the sum for state j of token t.
+// The states' halves are joined first, so that a token leaves one value behind.
+template <int NS, int STEP, int N>
+__device__ inline float join(const float (&v)[N], const Halves& h) {
+    if constexpr (N == 1) {
+        return v[0];
+    } else {
+        float to[N / 2];
 #pragma unroll
-    for (int i = 0; i < SelTile<NS>::NB; ++i) {
-        const int f = 16 * i + k, s = min(q * NS + f % NS, N - 1);
-        to[i] = One<T>::load(p + (int64_t)min(t0 + f / NS, n - 1) * stride + s);
+        for (int i = 0; i < N / 2; ++i) to[i] = halve<STEP>(v[i], v[i + N / 2], h);
+        return join<NS, STEP + 1>(to, h);
     }
 }
-template <typename T, int NS>
-__device__ inline void widen_states_of(const typename One<T>::raw (&r)[SelTile<NS>::NB], int t0, int n, int N, int q,
-                                       int k, float (&to)[SelTile<NS>::NB]) {
-#pragma unroll
-    for (int i = 0; i < SelTile<NS>::NB; ++i) {
-        const int f = 16 * i + k;
-        to[i] = q * NS + f % NS < N && t0 + f / NS < n ? One<T>::widen(r[i]) : 0.f;
-    }
+template <int NS>
+__device__ inline float join_states(const float (&v)[NS], const Halves& h) {
+    return join<NS, 0>(v, h);
 }
-// dy is of y's type, which may not be x's.
-template <typename T>
-__device__ inline float load_dy(const SelArgs& a, int64_t at) {
-    return a.y_f32 ? ((const float*)a.dy)[at] : One<bf16_t>::widen(One<bf16_t>::load((const bf16_t*)a.dy + at));
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+template <int NS>
+__device__ inline float join_tokens(const float (&v)[16 / NS], const Halves& h) {
+    return join<NS, log2_of(NS)>(v, h);
+}
+// The state and the token of lane l of a row.
+template <int NS>
+__device__ inline int joined_state(int l) {
+    return l / (16 / NS);
+}
+template <int NS>
+__device__ inline int joined_token(int l) {
+    return l % (16 / NS);
 }
 
 // ---------------------------------------------------------------- adjoints of items, from zero
 // The gradient that an item hands to the token before it if none enters at its end,
 // for all items but a sequence's first.
 template <typename T, int NS>
-__global__ __launch_bounds__(256) void selective_adjoint_kernel(SelArgs a, SelLayout lay, float* ends, float* steps) {
+__global__ __launch_bounds__(256, NS <= 4 ? 5 : 3) void selective_adjoint_kernel(SelArgs a, SelLayout lay, float* ends, float* steps) {
     typedef SelTile<NS> G;
     constexpr int TT = G::TT, Q = G::Q;
+    // what the rows of a wave hand to each other: step sizes and the output's gradient
+    __shared__ float s_x[4][TT][16][2];
     const int lane = threadIdx.x & 63, q = lane >> 4, k = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = a.C / a.G, nblk = (per + 4 * kSelChannels - 1) / (4 * kSelChannels) * a.G;
@@ -83,7 +103,7 @@ __global__ __launch_bounds__(256) void selective_adjoint_kernel(SelArgs a, SelLa
     for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
         const int64_t place = w / nblk;
         const int cb = (int)(w - place * nblk), g = cb / (nblk / a.G);
-        const SelItem e = sel_item(a.cu, a.nseq, a.L, a.T, lay.item, place);
+        const SelItem e = uniform_item(sel_item(a.cu, a.nseq, a.L, a.T, lay.item, place));
         if (e.seq < 0 || e.index == 0) continue;
         const int c0 = g * per + ((cb - g * (nblk / a.G)) * 4 + wave) * kSelChannels, end = (g + 1) * per;
         if (c0 >= end) continue;
@@ -94,45 +114,73 @@ __global__ __launch_bounds__(256) void selective_adjoint_kernel(SelArgs a, SelLa
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
             const int s = q * NS + j;
-            A[j] = s < a.N ? a.A[(int64_t)c * a.N + s] * kLog2e : 0.f;
+            A[j] = s < a.N ? decay_rate(a.A[(int64_t)c * a.N + s]) : 0.f;
             ga[j] = 0.f;
         }
         const StepSize step(a.act, c);
         float total = 0.f;
-        const T* dp = (const T*)a.dt + e.lo * a.dt_stride + c;
-        const T* zp = (const T*)a.z + e.lo * a.z_stride + c;
-        const T* cp = (const T*)a.Cm + e.lo * a.c_stride + g * a.N;
-        for (int t0 = (n - 1) / TT * TT; t0 >= 0; t0 -= TT) {
-            typename One<T>::raw rc[G::NB];
+        typedef RowsOf<TT> Rows;
+        const int size = (int)sizeof(T);
+        Rows dts(a.dt, e.lo, a.dt_stride, size, a.C, c, q), zs(a.z, e.lo, a.z_stride, size, a.C, c, q);
+        Rows dys(a.dy, e.lo, a.C, a.y_f32 ? 4 : 2, a.C, c, q);
+        StatesOf<T, G> cs(a.Cm, e.lo, a.c_stride, g * a.N, a.N, q, k);
+        struct Raw {
+            typename One<T>::raw dt[Q], z[Q], c[G::NB];
+            uint32_t dy[Q];
+        };
+        auto move = [&](int rows) {
+            dts.move(rows);
+            dys.move(rows);
+            cs.move(rows);
+            if (a.z) zs.move(rows);
+        };
+        auto load = [&](int left, Raw& r) {
+            const TileRows td = dts.tile(left), ty = dys.tile(left), tz = zs.tile(left);
+            cs.load(left, r.c);
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                r.dt[i] = One<T>::load(td.r, td.at(4 * i));
+                r.dy[i] = load_either(ty, 4 * i, a.y_f32);
+                if (a.z) r.z[i] = One<T>::load(tz.r, tz.at(4 * i));
+            }
+            move(-TT);
+        };
+        // the tile's first `left` tokens; a row behind them takes a step of 0, and its dy is 0
+        auto tile = [&](int left, const Raw& r) {
             float cc[G::NB];
-            load_states_of<T, NS>(cp, a.c_stride, t0, n, a.N, q, k, rc);
-            widen_states_of<T, NS>(rc, t0, n, a.N, q, k, cc);
-            unroll<Q>([&](auto group) {
-                constexpr int i = Q - 1 - decltype(group)::value;
-                if (t0 + 4 * i >= n) return;
-                const int t = t0 + 4 * i + q;
-                const bool there = t < n;
-                const int64_t row = min(t, n - 1);
-                const float dt = there ? step(One<T>::widen(One<T>::load(dp + row * a.dt_stride))) : 0.f;
-                float u = load_dy<T>(a, (e.lo + row) * a.C + c);
+            cs.widen(r.c, cc);
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                float dt = step(One<T>::widen(r.dt[i]));
+                if (left < TT) dt = 4 * i + q < left ? dt : 0.f;
+                float u = widen_either(r.dy[i], a.y_f32);
                 if (a.z) {
-                    const float z = One<T>::widen(One<T>::load(zp + row * a.z_stride));
+                    const float z = One<T>::widen(r.z[i]);
                     u *= z * sigmoid_f(z);
                 }
                 total += dt;
-                float dts[4], us[4];
-                rows_to_all(dt, dts);
-                rows_to_all(there ? u : 0.f, us);
-                unroll<4>([&](auto token) {
-                    constexpr int t = 3 - decltype(token)::value;
-                    if (t0 + 4 * i + t >= n) return;
-                    unroll<NS>([&](auto state) {
-                        constexpr int j = decltype(state)::value, f = (4 * i + t) * NS + j;
-                        ga[j] = __builtin_amdgcn_exp2f(dts[t] * A[j]) *
-                                __builtin_fmaf(row_lane<f % 16>(cc[f / 16]), us[t], ga[j]);
-                    });
-                });
+                *(f32x2*)s_x[wave][4 * i + q][k] = f32x2{dt, u};
+            }
+            in_wave_order();
+            f32x2 next = *(const f32x2*)s_x[wave][TT - 1][k];
+            unroll<TT>([&](auto token) {
+                constexpr int t = TT - 1 - decltype(token)::value;
+                const f32x2 now = next;
+                if (t > 0) next = *(const f32x2*)s_x[wave][t > 0 ? t - 1 : 0][k];
+                add_row<t * NS % 16>(ga, cc[t * NS / 16], now[1]);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) ga[j] *= __builtin_amdgcn_exp2f(now[0] * A[j]);
             });
+            in_wave_order();
+        };
+        Raw cur, nxt;
+        int t0 = (n - 1) / TT * TT;
+        move(t0);
+        load(n - t0, nxt);
+        for (; t0 >= 0; t0 -= TT) {
+            cur = nxt;
+            if (t0) load(TT, nxt);
+            tile(n - t0, cur);
         }
         total = sum_all_rows(total);
         if (!on) continue;
@@ -155,38 +203,48 @@ __global__ __launch_bounds__(256) void selective_carry_back_kernel(SelArgs a, Se
         if (items < 2) continue;
         const int c = (int)(at / padded), n = (int)(at - (int64_t)c * padded);
         const bool there = n < a.N;
-        const float A = there ? a.A[(int64_t)c * a.N + n] * kLog2e : 0.f;
-        float h = a.dfinal && there ? a.dfinal[(s * a.C + c) * a.N + n] : 0.f;
+        const float A = there ? decay_rate(a.A[(int64_t)c * a.N + n]) : 0.f;
+        const float h = a.dfinal && there ? a.dfinal[(s * a.C + c) * a.N + n] : 0.f;
         const int64_t place = sel_place(a.cu != nullptr, s, r.lo, a.L, lay.item) + items - 1;
-        float* p = ends + place * row + at;
-        const float* st = steps + place * a.C + c;
-        for (int64_t j = items - 1; j > 0; --j, p -= row, st -= a.C) {
-            h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * *st), h, *p);
-            *p = h;
-        }
+        carry(ends + place * row + at, -row, steps + place * a.C + c, -(int64_t)a.C, items - 1, A, h);
     }
 }
 
 // ---------------------------------------------------------------- gradients
 template <typename T, int NS>
-__global__ __launch_bounds__(64 * kWaves) void selective_backward_kernel(SelArgs a, SelLayout lay, const float* ends,
+struct RawBack {
+    typedef SelBack<NS> G;
+    typename One<T>::raw x[G::Q], dt[G::Q], z[G::Q], b[G::NB], c[G::NB];
+    uint32_t dy[G::Q];
+};
+
+template <typename T, int NS>
+__global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelArgs a, SelLayout lay, const float* ends,
                                                                          float* part_bc, float* part_a) {
-    typedef SelTile<NS> G;
-    constexpr int TT = G::TT, NB = G::NB, Q = G::Q;
-    __shared__ float s_h[kWaves][kSubs][NS][64];
+    typedef SelBack<NS> G;
+    constexpr int TT = G::TT, NB = G::NB, Q = G::Q, SUB = G::SUB, SUBS = (int)kSelStateRows / SUB;
+    constexpr int P = 16 / NS;  // tokens of a register of sums over channels
+    // a lane's own states entering every SUB tokens of a chunk; not its first ones
+    // where LDS would hold one workgroup a compute unit in place of two
+    constexpr int FIRST = NS <= 8 ? 0 : 1;
+    __shared__ float s_h[kWaves][SUBS - FIRST][NS][64];
+    // what the rows of a wave hand to each other: step sizes, they times x, and the
+    // gradient of what the gate multiplies
+    __shared__ f32x4 s_x[kWaves][TT][16];
     __shared__ float s_bc[2][kWaves][2][NB][64];
     const int lane = threadIdx.x & 63, q = lane >> 4, k = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Halves halves(k);
     const int per = a.C / a.G, gblk = (int)lay.blocks_bc, nblk = gblk * a.G;
     const int64_t work = lay.places * nblk;
     int buf = 0;
     for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
         const int64_t place = w / nblk;
         const int cb = (int)(w - place * nblk), g = cb / gblk, block = cb - g * gblk;
-        const SelItem e = sel_item(a.cu, a.nseq, a.L, a.T, lay.item, place);
-        const int c0 = g * per + (block * kWaves + wave) * kSelChannels, end = (g + 1) * per;
-        const bool on = c0 + k < end;
-        const int c = on ? c0 + k : end - 1;  // lanes without a channel: gradients of zero
+        const SelItem e = uniform_item(sel_item(a.cu, a.nseq, a.L, a.T, lay.item, place));
+        const int c0 = g * per + (block * kWaves + wave) * kSelChannels + k, end = (g + 1) * per;
+        const bool on = c0 < end;
+        const int c = on ? c0 : end - 1;  // lanes without a channel: gradients of zero
         const int n = e.seq < 0 ? 0 : (int)e.n;
         const int64_t chan = (int64_t)c * a.N;
 
@@ -194,7 +252,7 @@ __global__ __launch_bounds__(64 * kWaves) void selective_backward_kernel(SelArgs
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
             const int s = q * NS + j;
-            A[j] = s < a.N ? a.A[chan + s] * kLog2e : 0.f;
+            A[j] = s < a.N ? decay_rate(a.A[chan + s]) : 0.f;
             dA[j] = ga[j] = 0.f;
             if (e.seq < 0 || !on) continue;
             if (!e.last) ga[j] = ends[((place + 1) * a.C + c) * (4 * NS) + s];
@@ -204,173 +262,252 @@ __global__ __launch_bounds__(64 * kWaves) void selective_backward_kernel(SelArgs
         const float D = a.D ? a.D[c] : 0.f;
         float dD = 0.f, dbias = 0.f;
 
-        const T* xp = (const T*)a.x + e.lo * a.x_stride + c;
-        const T* dp = (const T*)a.dt + e.lo * a.dt_stride + c;
-        const T* zp = (const T*)a.z + e.lo * a.z_stride + c;
-        const T* bp = (const T*)a.B + e.lo * a.b_stride + g * a.N;
-        const T* cp = (const T*)a.Cm + e.lo * a.c_stride + g * a.N;
-
-        float h[NS];
-        // the states over the TT tokens from t0, which are all there
-        auto advance = [&](int t0) {
-            typename One<T>::raw rb[NB];
-            float b[NB];
-            load_states_of<T, NS>(bp, a.b_stride, t0, n, a.N, q, k, rb);
-            widen_states_of<T, NS>(rb, t0, n, a.N, q, k, b);
-            unroll<Q>([&](auto group) {
-                constexpr int i = decltype(group)::value;
-                const int64_t row = t0 + 4 * i + q;
-                const float dt = step(One<T>::widen(One<T>::load(dp + row * a.dt_stride)));
-                const float x = One<T>::widen(One<T>::load(xp + row * a.x_stride));
-                float dts[4], xs[4];
-                rows_to_all(dt, dts);
-                rows_to_all(on ? dt * x : 0.f, xs);
-                unroll<4>([&](auto token) {
-                    constexpr int t = decltype(token)::value;
-                    unroll<NS>([&](auto state) {
-                        constexpr int j = decltype(state)::value, f = (4 * i + t) * NS + j;
-                        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dts[t] * A[j]), h[j],
-                                              row_lane<f % 16>(b[f / 16]) * xs[t]);
-                    });
-                });
-            });
+        // at the tile that is loaded next
+        typedef RowsOf<TT> Rows;
+        const int size = (int)sizeof(T);
+        Rows xs(a.x, e.lo, a.x_stride, size, a.C, c, q), dts(a.dt, e.lo, a.dt_stride, size, a.C, c, q);
+        Rows zs(a.z, e.lo, a.z_stride, size, a.C, c, q), dys(a.dy, e.lo, a.C, a.y_f32 ? 4 : 2, a.C, c, q);
+        StatesOf<T, G> bs(a.B, e.lo, a.b_stride, g * a.N, a.N, q, k), cs(a.Cm, e.lo, a.c_stride, g * a.N, a.N, q, k);
+        auto move = [&](int rows) {
+            xs.move(rows);
+            dts.move(rows);
+            dys.move(rows);
+            bs.move(rows);
+            cs.move(rows);
+            if (a.z) zs.move(rows);
         };
-        // gradients of the tile of t0, h the state entering it
-        auto tile = [&](int t0, auto tail) {
-            constexpr bool TAIL = decltype(tail)::value;
-            typename One<T>::raw rb[NB], rc[NB];
-            float b[NB], cc[NB], x[Q], raw[Q], dt[Q], dy[Q], z[Q], u[Q];
-            load_states_of<T, NS>(bp, a.b_stride, t0, n, a.N, q, k, rb);
-            load_states_of<T, NS>(cp, a.c_stride, t0, n, a.N, q, k, rc);
-            widen_states_of<T, NS>(rb, t0, n, a.N, q, k, b);
-            widen_states_of<T, NS>(rc, t0, n, a.N, q, k, cc);
+        // ALL: or only what the states need
+        auto load = [&](int left, auto all, RawBack<T, NS>& r) {
+            const TileRows tx = xs.tile(left), td = dts.tile(left);
+            bs.load(left, r.b);
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
-                const int64_t row = min(t0 + 4 * i + q, n - 1);
-                const bool there = on && (!TAIL || t0 + 4 * i + q < n);
-                x[i] = there ? One<T>::widen(One<T>::load(xp + row * a.x_stride)) : 0.f;
-                raw[i] = One<T>::widen(One<T>::load(dp + row * a.dt_stride));
-                dt[i] = there ? step(raw[i]) : 0.f;
-                u[i] = dy[i] = there ? load_dy<T>(a, (e.lo + row) * a.C + c) : 0.f;
-                z[i] = 0.f;
-                if (a.z) {
-                    z[i] = there ? One<T>::widen(One<T>::load(zp + row * a.z_stride)) : 0.f;
-                    u[i] = dy[i] * (z[i] * sigmoid_f(z[i]));
-                }
+                r.x[i] = One<T>::load(tx.r, tx.at(4 * i));
+                r.dt[i] = One<T>::load(td.r, td.at(4 * i));
             }
-            float before[TT][NS], decay[TT][NS], last[NS];
-            unroll<Q>([&](auto group) {
-                constexpr int i = decltype(group)::value;
-                float dts[4], xs[4];
-                rows_to_all(dt[i], dts);
-                rows_to_all(dt[i] * x[i], xs);
-                unroll<4>([&](auto token) {
-                    constexpr int t = decltype(token)::value;
-                    unroll<NS>([&](auto state) {
-                        constexpr int j = decltype(state)::value, f = (4 * i + t) * NS + j;
-                        before[4 * i + t][j] = h[j];
-                        decay[4 * i + t][j] = 1.f;
-                        if (TAIL && t0 + 4 * i + t >= n) return;
-                        decay[4 * i + t][j] = __builtin_amdgcn_exp2f(dts[t] * A[j]);
-                        h[j] = __builtin_fmaf(decay[4 * i + t][j], h[j], row_lane<f % 16>(b[f / 16]) * xs[t]);
-                    });
-                });
-            });
+            if (!decltype(all)::value) return;
+            const TileRows ty = dys.tile(left), tz = zs.tile(left);
+            cs.load(left, r.c);
 #pragma unroll
-            for (int j = 0; j < NS; ++j) last[j] = h[j];
-            float pb[NB][16], pc[NB][16];
+            for (int i = 0; i < Q; ++i) {
+                r.dy[i] = load_either(ty, 4 * i, a.y_f32);
+                if (a.z) r.z[i] = One<T>::load(tz.r, tz.at(4 * i));
+            }
+        };
+        float h[NS];
+        // the states over the tile's TT tokens, which are all there
+        auto advance = [&](const RawBack<T, NS>& r) {
+            float b[NB];
+            bs.widen(r.b, b);
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float dt = step(One<T>::widen(r.dt[i]));
+                *(f32x2*)&s_x[wave][4 * i + q][k] = f32x2{dt, on ? dt * One<T>::widen(r.x[i]) : 0.f};
+            }
+            in_wave_order();
+            f32x2 next = *(const f32x2*)&s_x[wave][0][k];  // read one token ahead
+            unroll<TT>([&](auto token) {
+                constexpr int t = decltype(token)::value;
+                const f32x2 now = next;
+                if (t + 1 < TT) next = *(const f32x2*)&s_x[wave][t + 1 < TT ? t + 1 : 0][k];
+                unroll<NS>([&](auto state) {
+                    constexpr int j = decltype(state)::value, f = t * NS + j;
+                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(now[0] * A[j]), h[j],
+                                          row_lane<f % 16>(b[f / 16]) * now[1]);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            in_wave_order();
+        };
+        // gradients of the tile whose first row of the item is t0, `left` tokens of it, h
+        // the states entering it
+        auto tile = [&](int t0, int left, const RawBack<T, NS>& r, auto tail) {
+            constexpr bool TAIL = decltype(tail)::value;
+            float b[NB], cc[NB], dt[Q];
+            bs.widen(r.b, b);
+            cs.widen(r.c, cc);
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const bool there = on && (!TAIL || 4 * i + q < left);
+                dt[i] = there ? step(One<T>::widen(r.dt[i])) : 0.f;
+                float u = widen_either(r.dy[i], a.y_f32);
+                if (a.z) {
+                    const float z = One<T>::widen(r.z[i]);
+                    u *= z * sigmoid_f(z);
+                }
+                s_x[wave][4 * i + q][k] = f32x4{dt[i], there ? dt[i] * One<T>::widen(r.x[i]) : 0.f, there ? u : 0.f, 0.f};
+            }
+            in_wave_order();
+            float before[TT][NS], decay[TT][NS];
+            f32x4 next = s_x[wave][0][k];
+            __builtin_amdgcn_sched_barrier(0);
+            unroll<TT>([&](auto token) {
+                constexpr int t = decltype(token)::value;
+                const f32x4 here = next;
+                if (t + 1 < TT) next = s_x[wave][t + 1 < TT ? t + 1 : 0][k];
+                unroll<NS>([&](auto state) {
+                    constexpr int j = decltype(state)::value, f = t * NS + j;
+                    before[t][j] = h[j];
+                    decay[t][j] = 1.f;
+                    if (TAIL && t >= left) return;
+                    decay[t][j] = __builtin_amdgcn_exp2f(here[0] * A[j]);
+                    h[j] = __builtin_fmaf(decay[t][j], h[j], row_lane<f % 16>(b[f / 16]) * here[1]);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            auto to = [&](void* p, int64_t stride) {
+                Rows r(p, e.lo + t0, stride, size, a.C, c, q);
+                if (!on) r.lane = kSelNowhere;
+                return r.tile(left);
+            };
+            const TileRows gx = to(a.dx, a.dx_stride), gd = to(a.ddt, a.ddt_stride), gz = to(a.dz, a.dz_stride);
+            float pb[NB][P], pc[NB][P];
+            next = s_x[wave][TT - 1][k];
             unroll<Q>([&](auto group) {
                 constexpr int i = Q - 1 - decltype(group)::value;
-                float dts[4], xs[4], us[4], s[4], ew[4], y[4];
-                rows_to_all(dt[i], dts);
-                rows_to_all(dt[i] * x[i], xs);
-                rows_to_all(u[i], us);
+                float s[4], ew[4], y[4];
                 unroll<4>([&](auto token) {
-                    constexpr int t = 3 - decltype(token)::value, at = 4 * i + t;
+                    constexpr int t = 3 - decltype(token)::value, at = 4 * i + t, F = at * NS % 16;
+                    const f32x4 here = next;
+                    if (at > 0) next = s_x[wave][at > 0 ? at - 1 : 0][k];
                     s[t] = ew[t] = y[t] = 0.f;
-                    if (TAIL && t0 + at >= n) {
-                        unroll<NS>([&](auto state) {
-                            constexpr int f = at * NS + decltype(state)::value;
-                            pb[f / 16][f % 16] = pc[f / 16][f % 16] = 0.f;
-                        });
-                        return;
-                    }
-                    unroll<NS>([&](auto state) {
-                        constexpr int j = decltype(state)::value, f = at * NS + j;
-                        const float C = row_lane<f % 16>(cc[f / 16]);
-                        const float now = at + 1 < TT ? before[at + 1 < TT ? at + 1 : 0][j] : last[j];
-                        const float adj = __builtin_fmaf(us[t], C, ga[j]);
-                        pc[f / 16][f % 16] = us[t] * now;
-                        pb[f / 16][f % 16] = adj * xs[t];
-                        y[t] = __builtin_fmaf(C, now, y[t]);
-                        s[t] = __builtin_fmaf(row_lane<f % 16>(b[f / 16]), adj, s[t]);
-                        ga[j] = adj * decay[at][j];
+                    pb[at / P][at % P] = pc[at / P][at % P] = 0.f;
+                    if (TAIL && at >= left) return;
+                    // h: the states behind this token, ga: the adjoint in front of the next one
+                    float vb[NS], vc[NS];
+                    add_row<F>(ga, cc[at * NS / 16], here[2]);
+                    dot_row<F>(y[t], cc[at * NS / 16], h);
+                    dot_row<F>(s[t], b[at * NS / 16], ga);
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        vc[j] = here[2] * h[j];
+                        vb[j] = ga[j] * here[1];
+                        ga[j] *= decay[at][j];
                         const float wn = ga[j] * before[at][j];
                         ew[t] = __builtin_fmaf(wn, A[j], ew[t]);
-                        dA[j] = __builtin_fmaf(wn, dts[t], dA[j]);
-                    });
-                });
-                const float S = sum_rows(s), E = sum_rows(ew) * kLn2;
-                const float Y = a.z ? sum_rows(y) + D * x[i] : 0.f;
-                const bool there = on && (!TAIL || t0 + 4 * i + q < n);
-                if (there) {
-                    const int64_t row = e.lo + t0 + 4 * i + q;
-                    const float draw = (x[i] * S + E) * step.slope(raw[i], dt[i]);
-                    const bool f32 = std::is_same<T, float>::value;
-                    store_one(a.dx, row * a.dx_stride + c, f32, dt[i] * S + D * u[i]);
-                    store_one(a.ddt, row * a.ddt_stride + c, f32, draw);
-                    dbias += draw;
-                    dD += u[i] * x[i];
-                    if (a.z) {
-                        const float sg = sigmoid_f(z[i]);
-                        store_one(a.dz, row * a.dz_stride + c, f32, dy[i] * Y * (sg * (1.f + z[i] * (1.f - sg))));
+                        dA[j] = __builtin_fmaf(wn, here[0], dA[j]);
+                        h[j] = before[at][j];
                     }
+                    pb[at / P][at % P] = join_states<NS>(vb, halves);
+                    pc[at / P][at % P] = join_states<NS>(vc, halves);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                const bool there = on && (!TAIL || 4 * i + q < left);
+                const float S = sum_rows(s), E = sum_rows(ew) * kLn2;
+                const float x = there ? One<T>::widen(r.x[i]) : 0.f, dy = there ? widen_either(r.dy[i], a.y_f32) : 0.f;
+                float u = dy, dz = 0.f;
+                if (a.z) {
+                    const float z = there ? One<T>::widen(r.z[i]) : 0.f, sg = sigmoid_f(z);
+                    u *= z * sg;
+                    dz = dy * (sum_rows(y) + D * x) * (sg * (1.f + z * (1.f - sg)));
                 }
+                const float draw = there ? (x * S + E) * step.slope(One<T>::widen(r.dt[i]), dt[i]) : 0.f;
+                dbias += draw;
+                dD += u * x;
+                One<T>::store(gx.r, gx.at(4 * i), dt[i] * S + D * u);
+                One<T>::store(gd.r, gd.at(4 * i), draw);
+                if (a.z) One<T>::store(gz.r, gz.at(4 * i), dz);
+                // the sums over the wave's channels of the registers that are complete
+                unroll<NB>([&](auto reg) {
+                    constexpr int o = decltype(reg)::value;
+                    if constexpr (P * o >= 4 * i && P * o < 4 * i + 4) {
+                        s_bc[buf][wave][0][o][lane] = join_tokens<NS>(pb[o], halves);
+                        s_bc[buf][wave][1][o][lane] = join_tokens<NS>(pc[o], halves);
+                    }
+                });
+                __builtin_amdgcn_sched_barrier(0);
             });
-            // the workgroup's sums over its channels
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                s_bc[buf][wave][0][i][lane] = sum_channels(pb[i], k);
-                s_bc[buf][wave][1][i][lane] = sum_channels(pc[i], k);
-            }
-            __syncthreads();
+            // and over the workgroup's.  Only LDS is waited for: a barrier of the usual kind
+            // would also wait until the gradients just stored are in memory.
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             for (int o = threadIdx.x; o < 2 * NB * 64; o += 64 * kWaves) {
                 const int l = o & 63, i = (o >> 6) % NB, which = (o >> 6) / NB;
-                const int f = 16 * i + (l & 15), s = (l >> 4) * NS + f % NS, t = t0 + f / NS;
-                if (t >= n || s >= a.N) continue;
+                const int s = (l >> 4) * NS + joined_state<NS>(l & 15), t = P * i + joined_token<NS>(l & 15);
+                if (t >= left || s >= a.N) continue;
                 float v = 0.f;
 #pragma unroll
                 for (int o2 = 0; o2 < kWaves; ++o2) v += s_bc[buf][o2][which][i][l];
-                part_bc[(((int64_t)block * a.T + e.lo + t) * a.G + g) * (2 * a.N) + which * a.N + s] = v;
+                part_bc[(((int64_t)block * a.T + e.lo + t0 + t) * a.G + g) * (2 * a.N) + which * a.N + s] = v;
             }
             buf ^= 1;  // the readers of this one are done before the barrier after the next
         };
-        for (int chunk = n > 0 ? (n - 1) / (int)kSelStateRows * (int)kSelStateRows : -1; chunk >= 0;
-             chunk -= (int)kSelStateRows) {
+        int chunk = n > 0 ? (n - 1) / (int)kSelStateRows * (int)kSelStateRows : -1;
+        if (chunk > 0) move(chunk);
+        for (; chunk >= 0; chunk -= (int)kSelStateRows) {
             const int64_t slot = sel_place(a.cu != nullptr, e.seq, e.first, a.L, kSelStateRows) +
                                  (e.index * lay.item + chunk) / kSelStateRows;
+            const float* saved = a.states_in + slot * a.C * a.N + chan;
+            const int here = min(n - chunk, (int)kSelStateRows), subs = (here + SUB - 1) / SUB, ahead = (subs - 1) * SUB;
+            RawBack<T, NS> cur, nxt;
+            auto enter = [&] {
 #pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const int s = q * NS + j;
-                h[j] = on && s < a.N ? a.states_in[slot * a.C * a.N + chan + s] : 0.f;
-            }
-            const int subs = (min(n - chunk, (int)kSelStateRows) + kSub - 1) / kSub;
-            for (int sub = 0; sub < subs; ++sub) {
-                if (sub)
-                    for (int t = 0; t < kSub; t += TT) advance(chunk + (sub - 1) * kSub + t);
+                for (int j = 0; j < NS; ++j) {
+                    const int s = q * NS + j;
+                    h[j] = on && s < a.N ? saved[s] : 0.f;
+                }
+            };
+            auto keep = [&](int t) {  // the states entering token t of the chunk
+                if (t % SUB || t / SUB < FIRST) return;
 #pragma unroll
-                for (int j = 0; j < NS; ++j) s_h[wave][sub][j][lane] = h[j];
-            }
-            for (int sub = subs - 1; sub >= 0; --sub) {
-                const int base = chunk + sub * kSub, here = min(n - base, kSub);
-                for (int t = (here - 1) / TT * TT; t >= 0; t -= TT) {
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) h[j] = s_h[wave][sub][j][lane];
-                    for (int o = 0; o < t; o += TT) advance(base + o);
-                    if (t + TT <= here) tile(base + t, std::false_type{});
-                    else tile(base + t, std::true_type{});
+                for (int j = 0; j < NS; ++j) s_h[wave][t / SUB - FIRST][j][lane] = h[j];
+            };
+            enter();
+            constexpr int AHEAD = (SUBS - 1) * SUB / TT;  // tiles in front of a whole chunk's last SUB tokens
+            if (AHEAD <= 7 && subs == SUBS) {
+                // all of them in flight at once: the registers of a tile's states are still free
+                RawBack<T, NS> raw[AHEAD];
+                unroll<AHEAD>([&](auto o) {
+                    load(TT, std::false_type{}, raw[decltype(o)::value]);
+                    move(TT);
+                });
+                unroll<AHEAD>([&](auto o) {
+                    keep(decltype(o)::value * TT);
+                    advance(raw[decltype(o)::value]);
+                });
+            } else {
+                if (ahead) {
+                    load(TT, std::false_type{}, nxt);
+                    move(TT);
+                }
+                for (int t = 0; t < ahead; t += TT) {
+                    cur = nxt;
+                    if (t + TT < ahead) {
+                        load(TT, std::false_type{}, nxt);
+                        move(TT);
+                    }
+                    keep(t);
+                    advance(cur);
                 }
             }
+            keep(ahead);
+            int t = (here - 1) / TT * TT;
+            if (SUB > TT) move(t - ahead);
+            load(here - t, std::true_type{}, nxt);
+            for (; t >= 0; t -= TT) {
+                cur = nxt;
+                move(-TT);
+                if (t) load(TT, std::true_type{}, nxt);
+                if (t / SUB < FIRST) {
+                    enter();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) h[j] = s_h[wave][t / SUB - FIRST][j][lane];
+                }
+                if constexpr (SUB > TT) {  // from the state in LDS to this tile
+                    const int skip = t % SUB;
+                    move(TT - skip);
+                    for (int o = 0; o < skip; o += TT) {
+                        RawBack<T, NS> part;
+                        load(TT, std::false_type{}, part);
+                        move(TT);
+                        advance(part);
+                    }
+                    move(-TT);
+                }
+                if (t + TT <= here) tile(chunk + t, TT, cur, std::false_type{});
+                else tile(chunk + t, here - t, cur, std::true_type{});
+            }
+            move(TT - (int)kSelStateRows);
         }
         dD = sum_all_rows(dD);
         dbias = sum_all_rows(dbias);

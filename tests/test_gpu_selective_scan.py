@@ -22,6 +22,7 @@ CASES = [
     ([1, 700, 0, 63, 64, 65, 0], False, 72, 16, 1, "bf16", True, True, "bias", True, False),
     ([257, 3, 0, 129], False, 64, 11, 2, "f32", False, True, "clamp", True, True),
     ([200], True, 264, 8, 1, "f32", True, False, "bias", False, False),
+    ([95], False, 104, 16, 8, "bf16", True, True, "bias", True, False),
     ([77, 77, 77], True, 32, 7, 4, "bf16", False, True, "none", True, False),
     ([150, 2], False, 48, 32, 1, "f32", True, True, "bias", True, False),
     ([90], True, 56, 27, 1, "bf16", True, True, "bias", True, True),
