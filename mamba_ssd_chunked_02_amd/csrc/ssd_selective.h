@@ -284,16 +284,14 @@ __device__ inline float softplus_quick(float v) {
 struct StepSize {
     bool on, cut;
     float bias, lo, hi;
-    StepSize() = default;
     __device__ inline StepSize(const DtAct& a, int c) : on(a.on != 0), lo(a.lo), hi(a.hi) {
         cut = on && !(lo == 0.f && hi == __builtin_inff());
         bias = on && a.bias ? a.bias[c] : 0.f;
     }
     __device__ inline float operator()(float raw) const {
         if (!on) return raw;
-        float v = softplus_quick(raw + bias);
-        if (cut) v = v < lo ? lo : v > hi ? hi : v;
-        return v;
+        const float v = softplus_quick(raw + bias);
+        return __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, lo), hi);
     }
     // d step / d raw: 0 where the clamp cuts.
     __device__ inline float slope(float raw, float step) const {

@@ -186,51 +186,93 @@ __global__ __launch_bounds__(256) void selective_carry_kernel(SelArgs a, SelLayo
 }
 
 // ------------------------------------------------------------------ one token
-// Four lanes a channel, lane q of them the states q, q + 4, ... (VEC: 4 q + 0..3,
-// then 16 more, read as one vector); a few operations per byte of state: HBM.
+// A few operations per byte of state: HBM.  Four lanes a channel, lane q of them the
+// states 4 q .. 4 q + 3 of every sixteen; a lane takes kStepRows sequences, so that
+// their states are in flight together and A is read once for them.
+// VEC: states by fours, and A, B and C aligned to them.
+constexpr int kStepRows = 4;
+
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    __device__ static inline f32x4 load(const float* p) { return *(const f32x4*)p; }
+};
+template <>
+struct Four<bf16_t> {
+    __device__ static inline f32x4 load(const bf16_t* p) { return Raw<bf16_t>::widen(*(const Raw<bf16_t>::type*)p); }
+};
+template <typename T, bool VEC>
+__device__ inline f32x4 four_of(const T* p, int n, int N) {
+    if constexpr (VEC) return Four<T>::load(p + n);
+    f32x4 v = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (n + j < N) v[j] = One<T>::widen(One<T>::load(p + n + j));
+    return v;
+}
+
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, const float* state, float* state_out) {
-    const int64_t total = a.nseq * a.C;
-    const int q = threadIdx.x & 3, per = a.C / a.G;
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 2; i < total; i += (int64_t)gridDim.x * 64) {
-        const int64_t s = i / a.C;
-        const int c = (int)(i - s * a.C);
-        const float x = One<T>::widen(One<T>::load((const T*)a.x + s * a.x_stride + c));
-        const float dt = StepSize(a.act, c)(One<T>::widen(One<T>::load((const T*)a.dt + s * a.dt_stride + c)));
-        const T* bp = (const T*)a.B + s * a.b_stride + (int64_t)(c / per) * a.N;
-        const T* cp = (const T*)a.Cm + s * a.c_stride + (int64_t)(c / per) * a.N;
-        const float* Ap = a.A + (int64_t)c * a.N;
-        const float xs = dt * x;
-        float y = 0.f;
-        if constexpr (VEC) {
-            for (int n = 4 * q; n < a.N; n += 16) {
-                f32x4 h = *(const f32x4*)(state + i * a.N + n);
+    const int q = threadIdx.x & 3, blocks = (a.C + 63) / 64;
+    const int64_t groups = (a.nseq + kStepRows - 1) / kStepRows;
+    for (int64_t w = blockIdx.x; w < groups * blocks; w += gridDim.x) {
+        const int64_t s0 = w / blocks * kStepRows;
+        const int c = (int)(w % blocks) * 64 + (threadIdx.x >> 2);
+        if (c >= a.C) continue;  // the four lanes of a channel together
+        const int rows = (int)min(a.nseq - s0, (int64_t)kStepRows);
+        const int64_t first = (int64_t)(c / (a.C / a.G)) * a.N;  // of the channel's group
+        const StepSize step(a.act, c);
+        float x[kStepRows], dt[kStepRows], z[kStepRows], y[kStepRows];
+#pragma unroll
+        for (int r = 0; r < kStepRows; ++r) {
+            const int64_t s = s0 + min(r, rows - 1);
+            x[r] = One<T>::widen(One<T>::load((const T*)a.x + s * a.x_stride + c));
+            dt[r] = One<T>::widen(One<T>::load((const T*)a.dt + s * a.dt_stride + c));
+            z[r] = a.z ? One<T>::widen(One<T>::load((const T*)a.z + s * a.z_stride + c)) : 0.f;
+            y[r] = 0.f;
+        }
+        const float D = a.D ? a.D[c] : 0.f;
+        for (int n = 4 * q; n < a.N; n += 16) {
+            f32x4 A = four_of<float, VEC>(a.A + (int64_t)c * a.N, n, a.N), h[kStepRows], B[kStepRows], C[kStepRows];
+#pragma unroll
+            for (int r = 0; r < kStepRows; ++r) {
+                const int64_t s = s0 + min(r, rows - 1), at = (s * a.C + c) * a.N;
+                h[r] = four_of<float, VEC>(state + at, n, a.N);
+                B[r] = four_of<T, VEC>((const T*)a.B + s * a.b_stride + first, n, a.N);
+                C[r] = four_of<T, VEC>((const T*)a.Cm + s * a.c_stride + first, n, a.N);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) A[j] = decay_rate(A[j]);
+#pragma unroll
+            for (int r = 0; r < kStepRows; ++r) {
+                if (r >= rows) break;
+                const float d = step(dt[r]), xs = d * x[r];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * decay_rate(Ap[n + j])), h[j],
-                                          One<T>::widen(One<T>::load(bp + n + j)) * xs);
-                    y = __builtin_fmaf(One<T>::widen(One<T>::load(cp + n + j)), h[j], y);
+                    h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A[j]), h[r][j], B[r][j] * xs);
+                    if (VEC || n + j < a.N) y[r] = __builtin_fmaf(C[r][j], h[r][j], y[r]);
                 }
-                *(f32x4*)(state_out + i * a.N + n) = h;
-            }
-        } else {
-            for (int n = q; n < a.N; n += 4) {
-                const float h = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * decay_rate(Ap[n])), state[i * a.N + n],
-                                               One<T>::widen(One<T>::load(bp + n)) * xs);
-                y = __builtin_fmaf(One<T>::widen(One<T>::load(cp + n)), h, y);
-                state_out[i * a.N + n] = h;
+                float* to = state_out + ((s0 + r) * a.C + c) * a.N + n;
+                if constexpr (VEC) {
+                    *(f32x4*)to = h[r];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n + j < a.N) to[j] = h[r][j];
+                }
             }
         }
-        y += __shfl_xor(y, 1);
-        y += __shfl_xor(y, 2);
-        if (a.D) y += a.D[c] * x;
-        if (a.z) {
-            const float z = One<T>::widen(One<T>::load((const T*)a.z + s * a.z_stride + c));
-            y *= z * sigmoid_f(z);
-        }
-        if (q == 0) {
-            if (a.y_f32) ((float*)a.y)[i] = y;
-            else ((bf16_t*)a.y)[i] = (bf16_t)y;
+#pragma unroll
+        for (int r = 0; r < kStepRows; ++r) {
+            float v = y[r];
+            v += __shfl_xor(v, 1);
+            v += __shfl_xor(v, 2);
+            v += D * x[r];
+            if (a.z) v *= z[r] * sigmoid_f(z[r]);
+            if (q != 0 || r >= rows) continue;
+            if (a.y_f32) ((float*)a.y)[(s0 + r) * a.C + c] = v;
+            else ((bf16_t*)a.y)[(s0 + r) * a.C + c] = (bf16_t)v;
         }
     }
 }
@@ -273,11 +315,13 @@ hipError_t launch_selective_scan(const SelArgs& a, const SelLayout& lay, void* w
 }
 
 hipError_t launch_selective_step(const SelArgs& a, const float* state, float* state_out, hipStream_t stream) {
-    const int64_t total = a.nseq * a.C;
-    if (total == 0) return hipSuccess;
-    const dim3 grid((unsigned)std::min<int64_t>((total + 63) / 64, kMaxBlocks)), block(256);
+    const int64_t work = (a.nseq + kStepRows - 1) / kStepRows * ((a.C + 63) / 64);
+    if (work == 0) return hipSuccess;
+    const dim3 grid((unsigned)std::min<int64_t>(work, kMaxBlocks)), block(256);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, state, state_out); };
-    const bool vec = a.N % 4 == 0;
+    const uintptr_t four = a.dtype == 1 ? 8 : 16;
+    const bool vec = a.N % 4 == 0 && (uintptr_t)a.A % 16 == 0 && (uintptr_t)a.B % four == 0 && (uintptr_t)a.Cm % four == 0 &&
+                     a.b_stride % 4 == 0 && a.c_stride % 4 == 0;
     if (a.dtype == 1) vec ? go(selective_step_kernel<bf16_t, true>) : go(selective_step_kernel<bf16_t, false>);
     else vec ? go(selective_step_kernel<float, true>) : go(selective_step_kernel<float, false>);
     return hipGetLastError();

@@ -68,9 +68,33 @@ __device__ inline float join(const float (&v)[N], const Halves& h) {
         return join<NS, STEP + 1>(to, h);
     }
 }
+// Both gradients' NS states of a token, each in one value.  For four states the adds
+// write only the lanes of their half, 6 operations a value in place of 9; every
+// operand is written at least two instructions before its lanes are exchanged.
 template <int NS>
-__device__ inline float join_states(const float (&v)[NS], const Halves& h) {
-    return join<NS, 0>(v, h);
+__device__ inline void join_states(const float (&v)[NS], const float (&w)[NS], const Halves& h, float& tv, float& tw) {
+    if constexpr (NS == 4) {
+        float a, b, c, d;
+        asm("s_nop 1\n\t"
+            "v_add_f32_dpp %2, %6, %6 row_mirror row_mask:0xf bank_mask:0xf\n\t"
+            "v_add_f32_dpp %2, %8, %8 row_mirror row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %3, %7, %7 row_mirror row_mask:0xf bank_mask:0xf\n\t"
+            "v_add_f32_dpp %3, %9, %9 row_mirror row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %4, %10, %10 row_mirror row_mask:0xf bank_mask:0xf\n\t"
+            "v_add_f32_dpp %4, %12, %12 row_mirror row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %5, %11, %11 row_mirror row_mask:0xf bank_mask:0xf\n\t"
+            "v_add_f32_dpp %5, %13, %13 row_mirror row_mask:0xf bank_mask:0xc\n\t"
+            "v_add_f32_dpp %0, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+            "v_add_f32_dpp %0, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+            "v_add_f32_dpp %1, %4, %4 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+            "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+            "s_nop 1"
+            : "=&v"(tv), "=&v"(tw), "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+            : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]));
+    } else {
+        tv = join<NS, 0>(v, h);
+        tw = join<NS, 0>(w, h);
+    }
 }
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 template <int NS>
@@ -388,8 +412,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                         dA[j] = __builtin_fmaf(wn, here[0], dA[j]);
                         h[j] = before[at][j];
                     }
-                    pb[at / P][at % P] = join_states<NS>(vb, halves);
-                    pc[at / P][at % P] = join_states<NS>(vc, halves);
+                    join_states<NS>(vb, vc, halves, pb[at / P][at % P], pc[at / P][at % P]);
                     __builtin_amdgcn_sched_barrier(0);
                 });
                 const bool there = on && (!TAIL || 4 * i + q < left);
