@@ -430,8 +430,11 @@ SSD_API ssd_status ssd_gated_rms_norm_backward(const void* dy, const void* x, co
 // ------------------------------------------------------------------ layer norm
 namespace {
 
-// dweight's, dbias's and dscale's partial sums.
-size_t layer_norm_workspace(const ssd::NormArgs& a) { return (size_t)a.nparts * a.D * 12; }
+// dweight's, dbias's and dscale's partial sums, with a residual or without.
+size_t layer_norm_workspace(const ssd::NormArgs& a) {
+    const int32_t with = ssd::layer_norm_parts(a.rows, a.D, true), without = ssd::layer_norm_parts(a.rows, a.D, false);
+    return (size_t)(with > without ? with : without) * a.D * 12;
+}
 
 }  // namespace
 
@@ -520,5 +523,6 @@ SSD_API ssd_status ssd_layer_norm_backward(const void* dy, const void* dout, con
     a.dbias = dbias;
     a.dscale = dscale;
     a.part = (float*)workspace;
+    a.nparts = ssd::layer_norm_parts(a.rows, a.D, ssd::layer_norm_residual(a));
     return queued(ssd::launch_layer_norm_backward(a, (hipStream_t)stream));
 }

@@ -17,6 +17,11 @@ namespace ssd {
 namespace {
 
 constexpr int64_t kMaxBlocks = 1 << 22;  // a launch counts its lanes in 32 bits
+constexpr int kBackWaves = 10;           // of a workgroup of the backward pass
+
+// Vectors of 8 columns a lane of the backward pass: one up to 10 waves a row, else as few
+// as 8 waves allow.
+inline int backward_vectors(int n) { return n <= kBackWaves * 64 * kVec ? 1 : norm_vectors(n); }
 
 // ------------------------------------------------------------------ forward
 // A: type of x and y, B: of the residual (RES).
@@ -90,9 +95,13 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void layer_norm_kernel
 // Team k takes the rows k, k + teams, ..., the next one's data in flight, and keeps
 // its sums over rows in registers; a workgroup's go to its own row of the partial
 // sums, which a second kernel adds.
-template <typename A, typename B, int LANES, bool WIDE, int V>
-__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void layer_norm_backward_kernel(NormArgs a) {
-    __shared__ float lds[kMaxWaves][2];
+// RES: there may be a gradient of the sum, a scale and a second output.
+// Waves of a SIMD that the registers allow.
+constexpr int backward_waves(bool res, int V) { return V == 1 ? 4 : V == 2 && !res ? 3 : 2; }
+
+template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
+__global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxWaves, backward_waves(RES, V)) void layer_norm_backward_kernel(NormArgs a) {
+    __shared__ float lds[kBackWaves][2];
     __shared__ f32x4 sums[WIDE ? 1 : 3 * 64 * V * 2];
     constexpr bool SPLIT = sizeof(A) == 4 || sizeof(B) == 4;
     typedef Eight<A, SPLIT> EA;
@@ -100,7 +109,7 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void l
     typedef Eight<float, SPLIT> EW;
     const Team<LANES, WIDE, V> p;
     const int n = a.D;
-    const bool scaled = a.dscale;
+    const bool scaled = RES && a.dscale;
     struct Row {
         typename EA::raw dy[V], x[V];
         typename EB::raw u[V], dout[V];
@@ -115,18 +124,18 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void l
             const Cols k = p.template cols<SPLIT>(v, there ? n : 0);
             r.dy[v] = EA::load((const A*)a.dy + row * n, k);
             r.u[v] = EB::load((const B*)a.out + row * n, k);
+            if constexpr (!RES) continue;
             r.dout[v] = {};
             r.x[v] = {};
             if (a.dout) r.dout[v] = EB::load((const B*)a.dout + row * n, k);
             if (scaled) r.x[v] = EA::load((const A*)a.x + row * n, k);
         }
     };
-    f32x8 w[V], sc[V], acc[3][V] = {};  // dw, db, dscale
+    f32x8 w[V], dw[V] = {}, db[V] = {}, ds[V] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const Cols k = p.template cols<SPLIT>(v, n);
         w[v] = EW::cached(a.weight, k);
-        sc[v] = a.scale ? EW::cached(a.scale, k) : f32x8{1, 1, 1, 1, 1, 1, 1, 1};
     }
     constexpr bool kAhead = V < 4;  // there are no registers for the next row of the widest ones
     Row cur, nxt;
@@ -148,8 +157,8 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void l
             const f32x8 d = EA::widen(cur.dy[v]);
             m[v] = (EB::widen(cur.u[v]) - cur.mean) * cur.rstd;
             wd[v] = d * w[v];
-            acc[0][v] += d * m[v];
-            acc[1][v] += d;
+            dw[v] += d * m[v];
+            db[v] += d;
             mean1 += sum8(wd[v]);
             mean2 += sum8(wd[v] * m[v]);
         }
@@ -160,17 +169,18 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void l
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const Cols k = p.template cols<SPLIT>(v, n);
-            const f32x8 du = (wd[v] - mean1 - m[v] * mean2) * cur.rstd + EB::widen(cur.dout[v]);
-            if (a.dz) EB::store((B*)a.dz + row * n, k, du);
-            if (scaled) acc[2][v] += du * EA::widen(cur.x[v]);
-            EA::store((A*)a.dx + row * n, k, du * sc[v]);
+            f32x8 du = (wd[v] - mean1 - m[v] * mean2) * cur.rstd;
+            if constexpr (RES) {
+                du += EB::widen(cur.dout[v]);
+                if (a.dz) EB::store((B*)a.dz + row * n, k, du);
+                if (scaled) ds[v] += du * EA::widen(cur.x[v]);
+                if (a.scale) du *= EW::cached(a.scale, k);  // read again: registers are short
+            }
+            EA::store((A*)a.dx + row * n, k, du);
         }
     }
     // this workgroup's sums over its rows
-#pragma unroll
-    for (int o = 0; o < 3; ++o) {
-        if ((o == 1 && !a.dbias) || (o == 2 && !scaled)) continue;
-        f32x8(&s)[V] = acc[o];
+    auto out = [&](f32x8(&s)[V], int o) {
         float* to = a.part + ((int64_t)o * a.nparts + blockIdx.x) * n;
         if constexpr (!WIDE) {
             // the wave's teams hold the same columns; then waves 1..3 through LDS
@@ -190,7 +200,7 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void l
                 }
             }
             __syncthreads();
-            if (wave || lane >= LANES) continue;
+            if (wave || lane >= LANES) return;
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -201,7 +211,10 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256, V == 1 ? 4 : 2) void l
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) EW::store_cached(to, p.template cols<SPLIT>(v, n), s[v]);
-    }
+    };
+    out(dw, 0);
+    if (a.dbias) out(db, 1);
+    if (scaled) out(ds, 2);
 }
 
 // dweight, dbias and dscale (blockIdx.y: which of those wanted) from the workgroups' partial sums.
@@ -215,52 +228,91 @@ __global__ __launch_bounds__(kSumThreads) void layer_norm_sums_kernel(NormArgs a
 }
 
 template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
-hipError_t run_layer_norm(const NormArgs& a, bool backward, hipStream_t stream) {
-    const int threads = WIDE ? norm_threads(a.D, V) : 256;
-    if (backward) {
-        if (a.rows > 0) {
-            hipLaunchKernelGGL((layer_norm_backward_kernel<A, B, LANES, WIDE, V>), dim3(a.nparts), dim3(threads), 0, stream,
-                               a);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
-        hipLaunchKernelGGL(layer_norm_sums_kernel,
-                           dim3((a.D + kSumCols - 1) / kSumCols, 1 + (a.dbias != nullptr) + (a.dscale != nullptr)),
-                           dim3(kSumThreads), 0, stream, a, (int64_t)(a.rows > 0 ? a.nparts : 0));
-        return hipGetLastError();
-    }
-    const int64_t per = WIDE ? 1 : 256 / LANES;
+hipError_t run_forward(const NormArgs& a, hipStream_t stream) {
+    const int threads = WIDE ? norm_threads(a.D, V) : 256, per = WIDE ? 1 : 256 / LANES;
     if (a.rows == 0) return hipSuccess;
     const int64_t blocks = std::min<int64_t>((a.rows + per - 1) / per, kMaxBlocks);
     hipLaunchKernelGGL((layer_norm_kernel<A, B, RES, LANES, WIDE, V>), dim3((unsigned)blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
 }
 
+template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
+hipError_t run_backward(const NormArgs& a, hipStream_t stream) {
+    if (a.rows > 0) {
+        hipLaunchKernelGGL((layer_norm_backward_kernel<A, B, RES, LANES, WIDE, V>), dim3(a.nparts),
+                           dim3(WIDE ? norm_threads(a.D, V) : 256), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(layer_norm_sums_kernel,
+                       dim3((a.D + kSumCols - 1) / kSumCols, 1 + (a.dbias != nullptr) + (a.dscale != nullptr)),
+                       dim3(kSumThreads), 0, stream, a, (int64_t)(a.rows > 0 ? a.nparts : 0));
+    return hipGetLastError();
+}
+
+// Forward, rows of 513 to 2560 columns go to one wave each, which needs no barrier for
+// its two sums (65536 x 1536, bf16: 83 us, over a workgroup's waves 102; 32768 x 2560,
+// fp32: 113, 128); wider ones to two to four waves (16384 x 5120, bf16: two waves 77 us, one 83, five 87).
 template <typename A, typename B, bool RES>
-hipError_t by_columns(const NormArgs& a, bool backward, hipStream_t stream) {
+hipError_t forward_by_columns(const NormArgs& a, hipStream_t stream) {
     const int n = a.D;
-    if (n <= 8 * kVec) return run_layer_norm<A, B, RES, 8, false, 1>(a, backward, stream);
-    if (n <= 16 * kVec) return run_layer_norm<A, B, RES, 16, false, 1>(a, backward, stream);
-    if (n <= 32 * kVec) return run_layer_norm<A, B, RES, 32, false, 1>(a, backward, stream);
-    if (n <= 64 * kVec) return run_layer_norm<A, B, RES, 64, false, 1>(a, backward, stream);
-    switch (norm_vectors(n)) {
-        case 1: return run_layer_norm<A, B, RES, 64, true, 1>(a, backward, stream);
-        case 2: return run_layer_norm<A, B, RES, 64, true, 2>(a, backward, stream);
-        default: return run_layer_norm<A, B, RES, 64, true, 4>(a, backward, stream);
+    if (n <= 8 * kVec) return run_forward<A, B, RES, 8, false, 1>(a, stream);
+    if (n <= 16 * kVec) return run_forward<A, B, RES, 16, false, 1>(a, stream);
+    if (n <= 32 * kVec) return run_forward<A, B, RES, 32, false, 1>(a, stream);
+    if (n <= 64 * kVec) return run_forward<A, B, RES, 64, false, 1>(a, stream);
+    if (n <= 2 * 64 * kVec) return run_forward<A, B, RES, 64, false, 2>(a, stream);
+    if (n <= 3 * 64 * kVec) return run_forward<A, B, RES, 64, false, 3>(a, stream);
+    if (n <= 5 * 64 * kVec) return run_forward<A, B, RES, 64, false, 5>(a, stream);
+    if (n <= 8 * 64 * kVec) return run_forward<A, B, RES, 64, true, 4>(a, stream);
+    if (n <= 10 * 64 * kVec) return run_forward<A, B, RES, 64, true, 5>(a, stream);
+    if (n <= 16 * 64 * kVec) return run_forward<A, B, RES, 64, true, 4>(a, stream);
+    return run_forward<A, B, RES, 64, true, 4>(a, stream);
+}
+
+template <typename A, typename B, bool RES>
+hipError_t backward_by_columns(const NormArgs& a, hipStream_t stream) {
+    const int n = a.D;
+    if (n <= 8 * kVec) return run_backward<A, B, RES, 8, false, 1>(a, stream);
+    if (n <= 16 * kVec) return run_backward<A, B, RES, 16, false, 1>(a, stream);
+    if (n <= 32 * kVec) return run_backward<A, B, RES, 32, false, 1>(a, stream);
+    if (n <= 64 * kVec) return run_backward<A, B, RES, 64, false, 1>(a, stream);
+    switch (backward_vectors(n)) {
+        case 1: return run_backward<A, B, RES, 64, true, 1>(a, stream);
+        case 2: return run_backward<A, B, RES, 64, true, 2>(a, stream);
+        default: return run_backward<A, B, RES, 64, true, 4>(a, stream);
     }
 }
 
 }  // namespace
 
-hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
-    if (!a.z) return a.a_f32 ? by_columns<float, float, false>(a, false, stream) : by_columns<bf16_t, bf16_t, false>(a, false, stream);
-    if (a.a_f32) return by_columns<float, float, true>(a, false, stream);
-    return a.b_f32 ? by_columns<bf16_t, float, true>(a, false, stream) : by_columns<bf16_t, bf16_t, true>(a, false, stream);
+// Workgroups along the rows of the backward pass: what 256 compute units hold at once,
+// no more than there are rows for.
+int32_t layer_norm_parts(int64_t rows, int32_t D, bool res) {
+    const int V = backward_vectors(D), narrow = D <= 8 * kVec ? 8 : D <= 16 * kVec ? 16 : D <= 32 * kVec ? 32 : 64;
+    const bool wide = D > 64 * kVec;
+    const int per = wide ? 1 : 256 / narrow, waves = wide ? norm_threads(D, V) / 64 : 4;
+    const int held = 256 * std::max(1, 4 * backward_waves(res, V) / waves);
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, held));
 }
 
+hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
+    if (!a.z)
+        return a.a_f32 ? forward_by_columns<float, float, false>(a, stream)
+                       : forward_by_columns<bf16_t, bf16_t, false>(a, stream);
+    if (a.a_f32) return forward_by_columns<float, float, true>(a, stream);
+    return a.b_f32 ? forward_by_columns<bf16_t, float, true>(a, stream)
+                   : forward_by_columns<bf16_t, bf16_t, true>(a, stream);
+}
+
+bool layer_norm_residual(const NormArgs& a) { return a.dout || a.scale || a.dz || a.a_f32 != a.b_f32; }
+
 hipError_t launch_layer_norm_backward(const NormArgs& a, hipStream_t stream) {
-    if (a.a_f32) return by_columns<float, float, true>(a, true, stream);
-    return a.b_f32 ? by_columns<bf16_t, float, true>(a, true, stream) : by_columns<bf16_t, bf16_t, true>(a, true, stream);
+    const bool res = layer_norm_residual(a);
+    if (a.a_f32)
+        return res ? backward_by_columns<float, float, true>(a, stream) : backward_by_columns<float, float, false>(a, stream);
+    if (a.b_f32) return backward_by_columns<bf16_t, float, true>(a, stream);
+    return res ? backward_by_columns<bf16_t, bf16_t, true>(a, stream)
+               : backward_by_columns<bf16_t, bf16_t, false>(a, stream);
 }
 
 }  // namespace ssd
