@@ -45,10 +45,22 @@ def _state_stride(t, name) -> int:
     """Elements from one row [G, N] of t to the next, 0 where the rows are dense."""
     if t.is_contiguous():
         return 0
-    G, N = t.shape[-2:]
-    if (N > 1 and t.stride(-1) != 1) or (G > 1 and t.stride(-2) != N):
+    shape, strides = t.shape, t.stride()
+    G, N = shape[-2:]
+    if (N > 1 and strides[-1] != 1) or (G > 1 and strides[-2] != N):
         raise ValueError("the last two dimensions of %s must be dense" % name)
-    return _row_stride(t.as_strided(t.shape[:-2] + (G * N,), t.stride()[:-2] + (1,)), name)
+    rows, stride = 1, 0
+    for n, s in zip(shape[-3::-1], strides[-3::-1]):
+        if n == 1:
+            continue
+        if rows == 1:
+            stride = s
+        elif s != rows * stride:
+            raise ValueError("the rows of %s are not evenly spaced" % name)
+        rows *= n
+    if rows > 1 and stride < G * N:
+        raise ValueError("the rows of %s overlap" % name)
+    return stride if rows > 1 else 0
 
 
 def _activation(dt_softplus, dt_bias, dt_limit, C):
