@@ -14,9 +14,9 @@ namespace ssd {
 
 constexpr int kSumCols = 16, kSumStrips = 64, kSumThreads = kSumCols * kSumStrips;
 
-// at(row): the lane's column (blockIdx.x * kSumCols + threadIdx.x % kSumCols)
-// in that row, 0 if there is no such column.  The sum is returned in the first
-// kSumCols lanes.
+// at(row): the lane's column (threadIdx.x % kSumCols of the workgroup's) in that
+// row, 0 if there is no such column.  The sum is returned in the first kSumCols
+// lanes; a workgroup that takes columns again waits for all of them before.
 template <typename F>
 __device__ inline float column_sum(int64_t n, F at) {
     __shared__ float s_s[kSumStrips][kSumCols];

@@ -569,15 +569,17 @@ __global__ __launch_bounds__(256) void selective_sum_bc_kernel(SelArgs a, const 
 
 // dA, dD and dbias from the items' sums.
 __global__ __launch_bounds__(kSumThreads) void selective_sum_kernel(SelArgs a, const float* part, int64_t places) {
-    const int64_t width = (int64_t)a.C * (a.N + 2);
-    const int64_t col = (int64_t)blockIdx.x * kSumCols + threadIdx.x % kSumCols;
-    const float v = column_sum(places, [&](int64_t t) { return col < width ? part[t * width + col] : 0.f; });
-    if (threadIdx.x >= kSumCols || col >= width) return;
-    const int64_t states = (int64_t)a.C * a.N;
-    if (col < states) a.dA[col] = v;
-    else if (col < states + a.C) {
-        if (a.dD) a.dD[col - states] = v;
-    } else if (a.dbias) a.dbias[col - states - a.C] = v;
+    const int64_t width = (int64_t)a.C * (a.N + 2), states = (int64_t)a.C * a.N;
+    for (int64_t b = blockIdx.x; b < (width + kSumCols - 1) / kSumCols; b += gridDim.x) {
+        const int64_t col = b * kSumCols + threadIdx.x % kSumCols;
+        const float v = column_sum(places, [&](int64_t t) { return col < width ? part[t * width + col] : 0.f; });
+        __syncthreads();  // the sums of the columns before have been read
+        if (threadIdx.x >= kSumCols || col >= width) continue;
+        if (col < states) a.dA[col] = v;
+        else if (col < states + a.C) {
+            if (a.dD) a.dD[col - states] = v;
+        } else if (a.dbias) a.dbias[col - states - a.C] = v;
+    }
 }
 
 template <typename T, int NS>
@@ -611,8 +613,8 @@ hipError_t run_backward(const SelArgs& a, const SelLayout& lay, void* ws, hipStr
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }
-    const int64_t columns = (int64_t)a.C * (a.N + 2);
-    hipLaunchKernelGGL(selective_sum_kernel, dim3((unsigned)((columns + kSumCols - 1) / kSumCols)), dim3(kSumThreads), 0,
+    const int64_t blocks = ((int64_t)a.C * (a.N + 2) + kSumCols - 1) / kSumCols;
+    hipLaunchKernelGGL(selective_sum_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(kSumThreads), 0,
                        stream, a, part_a, lay.places);
     return hipGetLastError();
 }

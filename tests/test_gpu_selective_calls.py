@@ -238,3 +238,29 @@ def test_strided_steps():
         tol = 2.0 ** -7 * y[:, t].float().abs() + 400 * 2.0 ** -24 * y.float().abs().max()
         assert ((got.float() - y[:, t].float()).abs() <= tol).all(), t
     assert ((state - final).abs() <= 400 * 2.0 ** -24 * final.abs().max()).all()
+
+
+def test_most_channels():
+    """2^20 channels of 64 states: their sums take more workgroups than one launch holds lanes for."""
+    say("case: selective scan of 2^20 channels")
+    C, N, L, some = 1 << 20, 64, 3, 1024
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, dt, dy = (torch.randn(1, L, C, generator=g, device="cuda") for _ in range(3))
+    B, Cm = (torch.randn(1, L, 1, N, generator=g, device="cuda") for _ in range(2))
+    A = -torch.rand(C, N, generator=g, device="cuda") * 4
+    bias, D = (torch.randn(C, generator=g, device="cuda") for _ in range(2))
+    y, final, states = ssd.selective_scan(x, dt, A, B, Cm, D=D, dt_softplus=True, dt_bias=bias, want_states=True)
+    got = ssd.selective_scan_backward(dy, x, dt, A, B, Cm, states, D=D, dt_softplus=True, dt_bias=bias)
+    for at in (0, C // 2, C - some):
+        s = slice(at, at + some)
+        cut = [t[..., s].contiguous() for t in (dy, x, dt)]
+        kw = dict(D=D[s].contiguous(), dt_softplus=True, dt_bias=bias[s].contiguous())
+        y1, final1, st = ssd.selective_scan(cut[1], cut[2], A[s].contiguous(), B, Cm, want_states=True, **kw)
+        want = ssd.selective_scan_backward(*cut, A[s].contiguous(), B, Cm, st, **kw)
+        # a channel's values are the same operations in the same order wherever it stands
+        assert torch.equal(y[..., s], y1) and torch.equal(final[:, s], final1), at
+        for name, a, b in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "dbias"), got, want):
+            if name in ("dx", "ddt"):
+                assert torch.equal(a[..., s], b), (name, at)
+            elif name in ("dA", "dD", "dbias"):
+                assert torch.equal(a[s], b), (name, at)
