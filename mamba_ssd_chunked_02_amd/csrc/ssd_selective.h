@@ -141,19 +141,28 @@ __device__ inline void in_wave_order() {
     asm volatile("" ::: "memory");
 }
 
-// acc += src[lane F + j of its row] v[j] for j = 0..3: the multiplication takes its
-// operand across the row, which the compiler does only for plain products (with a
-// move otherwise: 7 cycles in place of 4.6).  The operand must not have been written
-// in the two instructions before.
-template <int F>
+// acc = (FIRST) or acc += src[lane F + j of its row] v[j] for j = 0..3: the
+// multiplication takes its operand across the row, which the compiler does only for
+// plain products (with a move otherwise: 7 cycles in place of 4.6).  The operand must
+// not have been written in the two instructions before.
+template <int F, bool FIRST>
 __device__ inline void dot_row4(float& acc, float src, float v0, float v1, float v2, float v3) {
-    asm("s_nop 1\n\t"
-        "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-        : "+v"(acc)
-        : "v"(src), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
+    if constexpr (FIRST)
+        asm("s_nop 1\n\t"
+            "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            : "=&v"(acc)
+            : "v"(src), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
+    else
+        asm("s_nop 1\n\t"
+            "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            : "+v"(acc)
+            : "v"(src), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
 }
 // acc_j += src[lane F + j of its row] v.
 template <int F>
@@ -166,13 +175,15 @@ __device__ inline void add_row4(float& a0, float& a1, float& a2, float& a3, floa
         : "+v"(a0), "+v"(a1), "+v"(a2), "+v"(a3)
         : "v"(src), "v"(v), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
 }
-// The same for the NS states of a token, whose first one is at lane F.
+// The same for the NS states of a token, whose first one is at lane F; the dot
+// product is returned.
 template <int F, int NS>
-__device__ inline void dot_row(float& acc, float src, const float (&v)[NS]) {
+__device__ inline float dot_row(float src, const float (&v)[NS]) {
+    float acc = 0.f;
     if constexpr (NS >= 4) {
         unroll<NS / 4>([&](auto four) {
             constexpr int o = 4 * decltype(four)::value;
-            dot_row4<F + o>(acc, src, v[o], v[o + 1], v[o + 2], v[o + 3]);
+            dot_row4<F + o, o == 0>(acc, src, v[o], v[o + 1], v[o + 2], v[o + 3]);
         });
     } else {
         unroll<NS>([&](auto one) {
@@ -180,6 +191,7 @@ __device__ inline void dot_row(float& acc, float src, const float (&v)[NS]) {
             acc = __builtin_fmaf(row_lane<F + j>(src), v[j], acc);
         });
     }
+    return acc;
 }
 template <int F, int NS>
 __device__ inline void add_row(float (&acc)[NS], float src, float v) {

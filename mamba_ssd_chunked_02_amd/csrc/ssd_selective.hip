@@ -119,8 +119,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
                         h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(now[0] * A[j]), h[j],
                                               row_lane<f % 16>(b[f / 16]) * now[1]);
                     });
-                    y[t] = 0.f;
-                    if constexpr (!LOCAL) dot_row<at * NS % 16>(y[t], cc[at * NS / 16], h);
+                    if constexpr (!LOCAL) y[t] = dot_row<at * NS % 16>(cc[at * NS / 16], h);
                 });
                 if constexpr (!LOCAL) {
                     float v = sum_rows(y) + D * One<T>::widen(r.x[i]);
