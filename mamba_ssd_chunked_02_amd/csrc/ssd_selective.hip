@@ -7,6 +7,15 @@
 // with and the sum S of its step sizes, a second carries the states over the items
 // (an item multiplies the state entering it by exp(A S)), a third writes y.  Where
 // the sequences alone fill the chip only the third runs.
+//
+// At 16 states the vector ALU bounds it, not HBM: 8.3 instructions a (token, channel,
+// state) here and 5.5 in the first launch, of which the exponential takes 8.4 cycles a
+// wave, its argument's product, the state's and y's 4 to 4.6 each.  Packed 49152
+// x 8192 x 16, bf16: y 1.64 ms (2.6 GB read, 0.86 written), the end states 1.10; 8 x
+// 2048 x 5120 x 16 as a whole 543 us, 2.5 T states a second where 8 waves a SIMD reach
+// 3.7: 2560 waves on 1024 SIMDs.  A wave's lanes are 16 channels by four quarters of
+// the states: by channel alone a lane would need 16 states, 64 channels' waves and
+// so four times the items, by state alone every load would serve one channel.
 #include <algorithm>
 #include <type_traits>
 
@@ -185,9 +194,11 @@ __global__ __launch_bounds__(256) void selective_carry_kernel(SelArgs a, SelLayo
 }
 
 // ------------------------------------------------------------------ one token
-// A few operations per byte of state: HBM.  Four lanes a channel, lane q of them the
-// states 4 q .. 4 q + 3 of every sixteen; a lane takes kStepRows sequences, so that
-// their states are in flight together and A is read once for them.
+// A few operations per byte of state: HBM, from a few MB of states on.  Four lanes a
+// channel, lane q of them the states 4 q .. 4 q + 3 of every sixteen; a lane takes
+// kStepRows sequences, so that their states are in flight together and A is read once
+// for them.  256 x 5120 x 16: 35 us, 176 MB, 5.0 TB/s; one
+// sequence of 1536 channels 4.7 us, which is a launch and one access' latency.
 // VEC: states by fours, and A, B and C aligned to them.
 constexpr int kStepRows = 4;
 
@@ -336,10 +347,11 @@ SelLayout sel_layout(const SelArgs& a, bool backward) {
     const int padded = a.N <= 4 ? 4 : a.N <= 8 ? 8 : a.N <= 16 ? 16 : a.N <= 32 ? 32 : 64;
     auto up = [](int64_t v) { return std::max<int64_t>((v + kSelStateRows - 1) / kSelStateRows, 1) * kSelStateRows; };
     // Forward: sequences of one length that bring 2 waves a SIMD go as a whole (8 x 2048 x
-    // 5120: 569 us; cut 650), else items for 16 waves a SIMD, so that their unequal ends
-    // even out (packed 49152 x 8192: 1024 tokens 3.03 ms, 512 and 2048 3.05, 6144 3.6),
-    // but 128 tokens at least (4096 x 1536: 64 tokens 88 us, 128 80, 256 107).  Backward:
-    // always items, since no sequence count that is common fills two waves a SIMD evenly.
+    // 5120: 564 us; cut into 512 tokens 640), else items for 16 waves a SIMD, so that their
+    // unequal ends even out (packed 49152 x 8192: 1024 tokens 2.98 ms, 512 3.04, 2048 3.02,
+    // 6144 3.31), but 128 tokens at least (4096 x 1536: 64 and 128 tokens 75 us, 256 96; 64
+    // take twice the workspace).  Backward: always items, since no sequence count that is
+    // common fills two waves a SIMD evenly (8 x 2048 x 5120 in items 1.93 ms, whole 2.23).
     const int64_t least = backward ? 64 : 128;
     if (!backward && !a.cu && a.nseq * waves >= 2048) l.item = up(a.L);
     else l.item = std::max(least, up((int64_t)((double)a.T * waves / 16384)));
