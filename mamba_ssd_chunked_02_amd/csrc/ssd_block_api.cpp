@@ -430,10 +430,12 @@ SSD_API ssd_status ssd_gated_rms_norm_backward(const void* dy, const void* x, co
 // ------------------------------------------------------------------ layer norm
 namespace {
 
-// dweight's, dbias's and dscale's partial sums, with a residual or without.
+// dweight's, dbias's and dscale's partial sums, for the kind that has the most workgroups.
 size_t layer_norm_workspace(const ssd::NormArgs& a) {
-    const int32_t with = ssd::layer_norm_parts(a.rows, a.D, true), without = ssd::layer_norm_parts(a.rows, a.D, false);
-    return (size_t)(with > without ? with : without) * a.D * 12;
+    int32_t parts = 0;
+    for (int kind : {ssd::kNormPlain, ssd::kNormResidual, ssd::kNormScaled})
+        for (bool f32 : {false, true}) parts = std::max(parts, ssd::layer_norm_parts(a.rows, a.D, kind, f32));
+    return (size_t)parts * a.D * 12;
 }
 
 }  // namespace
@@ -523,6 +525,6 @@ SSD_API ssd_status ssd_layer_norm_backward(const void* dy, const void* dout, con
     a.dbias = dbias;
     a.dscale = dscale;
     a.part = (float*)workspace;
-    a.nparts = ssd::layer_norm_parts(a.rows, a.D, ssd::layer_norm_residual(a));
+    a.nparts = ssd::layer_norm_parts(a.rows, a.D, ssd::layer_norm_kind(a), a.a_f32);
     return queued(ssd::launch_layer_norm_backward(a, (hipStream_t)stream));
 }

@@ -352,10 +352,11 @@ constexpr int32_t kMaxNormColumns = 16384;
 int32_t norm_parts(int64_t rows, int32_t D, int32_t G);
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_residual_norm_backward(const NormArgs& a, hipStream_t stream);
-// Layer norm: z and out are NULL without a residual.  Its backward pass, from the
-// arguments: whether it needs the kernel for residuals, and its workgroups along the rows.
-bool layer_norm_residual(const NormArgs& a);
-int32_t layer_norm_parts(int64_t rows, int32_t D, bool res);
+// Layer norm: z and out are NULL without a residual.  Its backward pass: which kind of
+// kernel the arguments need, and that one's workgroups along the rows.
+constexpr int kNormPlain = 0, kNormResidual = 1, kNormScaled = 2;
+int layer_norm_kind(const NormArgs& a);
+int32_t layer_norm_parts(int64_t rows, int32_t D, int kind, bool f32);
 hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_layer_norm_backward(const NormArgs& a, hipStream_t stream);
 hipError_t launch_gated_norm(const NormArgs& a, hipStream_t stream);

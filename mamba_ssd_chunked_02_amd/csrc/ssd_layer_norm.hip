@@ -3,8 +3,8 @@
 // with rstd = 1 / sqrt(mean((u - mean(u))^2) + eps) per row.
 // A few operations per element read: HBM streams.  A row is held in registers
 // between its sums and its use, so every input is read once.  65536 x 2560, bf16 with
-// an fp32 residual: forward 342 us, backward 688 (5.9 and 4.4 TB/s); 16384 x 5120, bf16:
-// 73 and 123 us (4.6 and 4.1).
+// an fp32 residual: forward 334 us, backward 481 (6.0 and 5.6 TB/s), with a scale 527 (5.7);
+// 16384 x 5120, bf16: 77 and 125 us (4.4 and 4.0).
 //
 // The mean is taken first and the squares of the distances from it then, both from
 // registers: a row whose mean is large against its spread keeps its digits.  The
@@ -21,9 +21,11 @@ namespace {
 constexpr int64_t kMaxBlocks = 1 << 22;  // a launch counts its lanes in 32 bits
 constexpr int kBackWaves = 10;           // of a workgroup of the backward pass
 
-// Vectors of 8 columns a lane of the backward pass: one up to 10 waves a row, else as few
-// as 8 waves allow.
-inline int backward_vectors(int n) { return n <= kBackWaves * 64 * kVec ? 1 : norm_vectors(n); }
+// Vectors of 8 columns a lane of the backward pass: one up to 8 waves a row (10 with a
+// residual), else as few as 8 waves allow.  16384 x 5120, bf16: two vectors 125 us, one 144.
+inline int backward_vectors(int n, int kind) {
+    return n <= (kind == kNormPlain ? 8 : kBackWaves) * 64 * kVec ? 1 : norm_vectors(n);
+}
 
 // ------------------------------------------------------------------ forward
 // A: type of x and y, B: of the residual (RES).
@@ -94,16 +96,24 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void layer_norm_kernel
 // With m = (u - mean) rstd and d the gradient of y:
 //   du = dout + rstd (w d - mean(w d) - m mean(w d m)),  dx = scale du,
 //   dw = sum over rows of d m,  db of d,  dscale of du x.
-// Team k takes the rows k, k + teams, ..., the next one's data in flight, and keeps
+// Team k takes the rows k, k + teams, ..., mostly with the next one's data in flight, and keeps
 // its sums over rows in registers; a workgroup's go to its own row of the partial
 // sums, which a second kernel adds.
 
-// Waves of a SIMD that the registers allow.
-constexpr int backward_waves(bool res, int V) { return V == 1 ? 4 : V == 2 && !res ? 3 : 2; }
+// Waves of a SIMD, and so registers a lane and workgroups at once.  With a residual
+// three, since the compiler at four waits for its loads early (65536 x 2560 bf16: 281
+// us, four 347; with an fp32 residual 480, 519), and with a scale none of the next row's
+// (527; with them 685, four waves without them 610).  fp32 without a residual: three
+// for one vector a lane (32768 x 2560: 168, four 195), four for two (16384 x 5120: 199,
+// 208); bf16 four (16384 x 4096: 83, three 108; 16384 x 8192 147, three with the next row 180).
+constexpr int backward_waves(int kind, bool f32, int V) {
+    return kind == kNormPlain && V <= 2 ? (V == 1 && f32 ? 3 : 4) : V == 1 ? 3 : 2;
+}
 
-// RES: there may be a gradient of the sum, a scale and a second output.
-template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
-__global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxWaves, backward_waves(RES, V)) void layer_norm_backward_kernel(NormArgs a) {
+// KIND: kNormResidual, there may be a gradient of the sum and a second output; kNormScaled, a scale too.
+template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
+__global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxWaves,
+                             backward_waves(KIND, sizeof(A) == 4, V)) void layer_norm_backward_kernel(NormArgs a) {
     __shared__ float lds[kBackWaves][2];
     __shared__ f32x4 sums[WIDE ? 1 : 3 * 64 * V * 2];
     constexpr bool SPLIT = sizeof(A) == 4 || sizeof(B) == 4;
@@ -112,7 +122,7 @@ __global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxW
     typedef Eight<float, SPLIT> EW;
     const Team<LANES, WIDE, V> p;
     const int n = a.D;
-    const bool scaled = RES && a.dscale;
+    const bool scaled = KIND == kNormScaled && a.dscale;
     struct Row {
         typename EA::raw dy[V], x[V];
         typename EB::raw u[V], dout[V];
@@ -127,7 +137,7 @@ __global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxW
             const Cols k = p.template cols<SPLIT>(v, there ? n : 0);
             r.dy[v] = EA::load((const A*)a.dy + row * n, k);
             r.u[v] = EB::load((const B*)a.out + row * n, k);
-            if constexpr (!RES) continue;
+            if constexpr (KIND == kNormPlain) continue;
             r.dout[v] = {};
             r.x[v] = {};
             if (a.dout) r.dout[v] = EB::load((const B*)a.dout + row * n, k);
@@ -140,7 +150,7 @@ __global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxW
         const Cols k = p.template cols<SPLIT>(v, n);
         w[v] = EW::cached(a.weight, k);
     }
-    constexpr bool kAhead = V < 4;  // there are no registers for the next row of the widest ones
+    constexpr bool kAhead = V == 1 ? KIND != kNormScaled : V == 2 && KIND == kNormResidual;  // the next row's loads
     Row cur, nxt;
     if (kAhead) load(p.index, nxt);
     // WIDE: the same rows for the whole workgroup; else as many rounds as the
@@ -173,11 +183,11 @@ __global__ __launch_bounds__(!WIDE ? 256 : V == 1 ? 64 * kBackWaves : 64 * kMaxW
         for (int v = 0; v < V; ++v) {
             const Cols k = p.template cols<SPLIT>(v, n);
             f32x8 du = (wd[v] - mean1 - m[v] * mean2) * cur.rstd;
-            if constexpr (RES) {
+            if constexpr (KIND != kNormPlain) {
                 du += EB::widen(cur.dout[v]);
                 if (a.dz) EB::store((B*)a.dz + row * n, k, du);
                 if (scaled) ds[v] += du * EA::widen(cur.x[v]);
-                if (a.scale) du *= EW::cached(a.scale, k);  // read again: registers are short
+                if constexpr (KIND == kNormScaled) du *= EW::cached(a.scale, k);  // read again: registers are short
             }
             EA::store((A*)a.dx + row * n, k, du);
         }
@@ -239,10 +249,10 @@ hipError_t run_forward(const NormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename A, typename B, bool RES, int LANES, bool WIDE, int V>
+template <typename A, typename B, int KIND, int LANES, bool WIDE, int V>
 hipError_t run_backward(const NormArgs& a, hipStream_t stream) {
     if (a.rows > 0) {
-        hipLaunchKernelGGL((layer_norm_backward_kernel<A, B, RES, LANES, WIDE, V>), dim3(a.nparts),
+        hipLaunchKernelGGL((layer_norm_backward_kernel<A, B, KIND, LANES, WIDE, V>), dim3(a.nparts),
                            dim3(WIDE ? norm_threads(a.D, V) : 256), 0, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -271,17 +281,17 @@ hipError_t forward_by_columns(const NormArgs& a, hipStream_t stream) {
     return run_forward<A, B, RES, 64, true, 4>(a, stream);
 }
 
-template <typename A, typename B, bool RES>
+template <typename A, typename B, int KIND>
 hipError_t backward_by_columns(const NormArgs& a, hipStream_t stream) {
     const int n = a.D;
-    if (n <= 8 * kVec) return run_backward<A, B, RES, 8, false, 1>(a, stream);
-    if (n <= 16 * kVec) return run_backward<A, B, RES, 16, false, 1>(a, stream);
-    if (n <= 32 * kVec) return run_backward<A, B, RES, 32, false, 1>(a, stream);
-    if (n <= 64 * kVec) return run_backward<A, B, RES, 64, false, 1>(a, stream);
-    switch (backward_vectors(n)) {
-        case 1: return run_backward<A, B, RES, 64, true, 1>(a, stream);
-        case 2: return run_backward<A, B, RES, 64, true, 2>(a, stream);
-        default: return run_backward<A, B, RES, 64, true, 4>(a, stream);
+    if (n <= 8 * kVec) return run_backward<A, B, KIND, 8, false, 1>(a, stream);
+    if (n <= 16 * kVec) return run_backward<A, B, KIND, 16, false, 1>(a, stream);
+    if (n <= 32 * kVec) return run_backward<A, B, KIND, 32, false, 1>(a, stream);
+    if (n <= 64 * kVec) return run_backward<A, B, KIND, 64, false, 1>(a, stream);
+    switch (backward_vectors(n, KIND)) {
+        case 1: return run_backward<A, B, KIND, 64, true, 1>(a, stream);
+        case 2: return run_backward<A, B, KIND, 64, true, 2>(a, stream);
+        default: return run_backward<A, B, KIND, 64, true, 4>(a, stream);
     }
 }
 
@@ -289,11 +299,11 @@ hipError_t backward_by_columns(const NormArgs& a, hipStream_t stream) {
 
 // Workgroups along the rows of the backward pass: what 256 compute units hold at once,
 // no more than there are rows for.
-int32_t layer_norm_parts(int64_t rows, int32_t D, bool res) {
-    const int V = backward_vectors(D), narrow = D <= 8 * kVec ? 8 : D <= 16 * kVec ? 16 : D <= 32 * kVec ? 32 : 64;
+int32_t layer_norm_parts(int64_t rows, int32_t D, int kind, bool f32) {
+    const int V = backward_vectors(D, kind), narrow = D <= 8 * kVec ? 8 : D <= 16 * kVec ? 16 : D <= 32 * kVec ? 32 : 64;
     const bool wide = D > 64 * kVec;
     const int per = wide ? 1 : 256 / narrow, waves = wide ? norm_threads(D, V) / 64 : 4;
-    const int held = 256 * std::max(1, 4 * backward_waves(res, V) / waves);
+    const int held = 256 * std::max(1, 4 * backward_waves(kind, f32, V) / waves);
     return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, held));
 }
 
@@ -306,15 +316,22 @@ hipError_t launch_layer_norm(const NormArgs& a, hipStream_t stream) {
                    : forward_by_columns<bf16_t, bf16_t, true>(a, stream);
 }
 
-bool layer_norm_residual(const NormArgs& a) { return a.dout || a.scale || a.dz || a.a_f32 != a.b_f32; }
+int layer_norm_kind(const NormArgs& a) {
+    return a.scale ? kNormScaled : a.dout || a.dz || a.a_f32 != a.b_f32 ? kNormResidual : kNormPlain;
+}
 
 hipError_t launch_layer_norm_backward(const NormArgs& a, hipStream_t stream) {
-    const bool res = layer_norm_residual(a);
+    const int kind = layer_norm_kind(a);
     if (a.a_f32)
-        return res ? backward_by_columns<float, float, true>(a, stream) : backward_by_columns<float, float, false>(a, stream);
-    if (a.b_f32) return backward_by_columns<bf16_t, float, true>(a, stream);
-    return res ? backward_by_columns<bf16_t, bf16_t, true>(a, stream)
-               : backward_by_columns<bf16_t, bf16_t, false>(a, stream);
+        return kind == kNormPlain      ? backward_by_columns<float, float, kNormPlain>(a, stream)
+               : kind == kNormResidual ? backward_by_columns<float, float, kNormResidual>(a, stream)
+                                   : backward_by_columns<float, float, kNormScaled>(a, stream);
+    if (a.b_f32)
+        return kind == kNormResidual ? backward_by_columns<bf16_t, float, kNormResidual>(a, stream)
+                                 : backward_by_columns<bf16_t, float, kNormScaled>(a, stream);
+    return kind == kNormPlain      ? backward_by_columns<bf16_t, bf16_t, kNormPlain>(a, stream)
+           : kind == kNormResidual ? backward_by_columns<bf16_t, bf16_t, kNormResidual>(a, stream)
+                               : backward_by_columns<bf16_t, bf16_t, kNormScaled>(a, stream);
 }
 
 }  // namespace ssd
