@@ -8,11 +8,11 @@
 // (an item multiplies the state entering it by exp(A S)), a third writes y.  Where
 // the sequences alone fill the chip only the third runs.
 //
-// At 16 states the vector ALU bounds it, not HBM: 8.3 instructions a (token, channel,
+// At 16 states the vector ALU bounds it, not HBM: 8.2 instructions a (token, channel,
 // state) here and 5.5 in the first launch, of which the exponential takes 8.4 cycles a
 // wave, its argument's product, the state's and y's 4 to 4.6 each.  Packed 49152
 // x 8192 x 16, bf16: y 1.64 ms (2.6 GB read, 0.86 written), the end states 1.10; 8 x
-// 2048 x 5120 x 16 as a whole 543 us, 2.5 T states a second where 8 waves a SIMD reach
+// 2048 x 5120 x 16 as a whole 535 us, 2.5 T states a second where 8 waves a SIMD reach
 // 3.7: 2560 waves on 1024 SIMDs.  A wave's lanes are 16 channels by four quarters of
 // the states: by channel alone a lane would need 16 states, 64 channels' waves and
 // so four times the items, by state alone every load would serve one channel.

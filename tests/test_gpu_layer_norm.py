@@ -38,6 +38,17 @@ CASES = [
     (600, 264, "bf16", None, True, False),
     (0, 64, "bf16", "bf16", True, True),
     (0, 64, "f32", None, True, False),
+    # several rows a workgroup of the gradients, of each kind and width
+    (2100, 1536, "bf16", None, True, False),
+    (1100, 2560, "f32", None, True, False),
+    (2100, 1536, "bf16", "bf16", True, False),
+    (2100, 1536, "bf16", "f32", True, True),
+    (1100, 5128, "bf16", None, True, False),
+    (1100, 5128, "f32", None, False, False),
+    (530, 5128, "bf16", "f32", True, False),
+    (530, 5128, "bf16", "bf16", True, True),
+    (530, 8200, "bf16", None, True, False),
+    (530, 8200, "f32", "f32", True, True),
 ]
 
 
