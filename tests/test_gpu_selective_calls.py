@@ -264,3 +264,16 @@ def test_most_channels():
                 assert torch.equal(a[..., s], b), (name, at)
             elif name in ("dA", "dD", "dbias"):
                 assert torch.equal(a[s], b), (name, at)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_of_the_other_type(dtype):
+    """dy in fp32 or bf16, whatever x is: a bf16 value is the same number in both."""
+    say("case: selective scan dy's type", dtype)
+    c = a_case([131, 0, 66], 40, 16, dtype)
+    *_, states = ssd.selective_scan(*c.args, **c.kw, want_states=True)
+    dy = torch.randn(c.x.shape, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda").bfloat16()
+    one = ssd.selective_scan_backward(dy, *c.args, states, **c.kw)
+    two = ssd.selective_scan_backward(dy.float(), *c.args, states, **c.kw)
+    for a, b in zip(one, two):
+        assert a is None and b is None or torch.equal(a, b)

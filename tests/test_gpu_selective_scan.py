@@ -32,6 +32,8 @@ CASES = [
     ([0, 0], False, 16, 16, 1, "bf16", True, True, "bias", True, False),
     ([0, 0], True, 16, 16, 1, "f32", True, True, "bias", True, False),
     ([], False, 16, 16, 1, "f32", True, True, "bias", True, False),
+    ([7 * k % 5 for k in range(1500)], False, 8, 16, 1, "bf16", True, True, "bias", True, False),
+    ([2] * 700, True, 24, 3, 3, "f32", True, True, "bias", True, False),
 ]
 
 
