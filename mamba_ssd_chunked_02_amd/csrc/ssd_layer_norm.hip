@@ -4,7 +4,7 @@
 // A few operations per element read: HBM streams.  A row is held in registers
 // between its sums and its use, so every input is read once.  65536 x 2560, bf16 with
 // an fp32 residual: forward 334 us, backward 481 (6.0 and 5.6 TB/s), with a scale 527 (5.7);
-// 16384 x 5120, bf16: 77 and 125 us (4.4 and 4.0).
+// 16384 x 5120, bf16: 77 and 102 us (4.4 and 4.9).
 //
 // The mean is taken first and the squares of the distances from it then, both from
 // registers: a row whose mean is large against its spread keeps its digits.  The
@@ -22,7 +22,7 @@ constexpr int64_t kMaxBlocks = 1 << 22;  // a launch counts its lanes in 32 bits
 constexpr int kBackWaves = 10;           // of a workgroup of the backward pass
 
 // Vectors of 8 columns a lane of the backward pass: one up to 8 waves a row (10 with a
-// residual), else as few as 8 waves allow.  16384 x 5120, bf16: two vectors 125 us, one 144.
+// residual), else as few as 8 waves allow.  16384 x 5120, bf16: two vectors 102 us, one 144.
 inline int backward_vectors(int n, int kind) {
     return n <= (kind == kNormPlain ? 8 : kBackWaves) * 64 * kVec ? 1 : norm_vectors(n);
 }
@@ -104,8 +104,8 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void layer_norm_kernel
 // three, since the compiler at four waits for its loads early (65536 x 2560 bf16: 281
 // us, four 347; with an fp32 residual 480, 519), and with a scale none of the next row's
 // (527; with them 685, four waves without them 610).  fp32 without a residual: three
-// for one vector a lane (32768 x 2560: 168, four 195), four for two (16384 x 5120: 199,
-// 208); bf16 four (16384 x 4096: 83, three 108; 16384 x 8192 147, three with the next row 180).
+// for one vector a lane (65536 x 1024: 138, four 149), four for two (16384 x 5120: 176,
+// three 208); bf16 four (16384 x 4096: 83, three 108; 16384 x 8192 147, three with the next row 180).
 constexpr int backward_waves(int kind, bool f32, int V) {
     return kind == kNormPlain && V <= 2 ? (V == 1 && f32 ? 3 : 4) : V == 1 ? 3 : 2;
 }
@@ -298,12 +298,17 @@ hipError_t backward_by_columns(const NormArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Workgroups along the rows of the backward pass: what 256 compute units hold at once,
-// no more than there are rows for.
+// no more than there are rows for.  Of each a power of two, so that rows divide evenly
+// (16384 x 5120 bf16: 2 102 us, 3 126; fp32 176, 200; 65536 x 1024 with an fp32 residual
+// 4 189, 6 209), but all of them for bf16 rows without a residual by one vector, which
+// have the least in flight (32768 x 2560: 3 99, 2 121; 65536 x 1536: 5 112, 4 120).
 int32_t layer_norm_parts(int64_t rows, int32_t D, int kind, bool f32) {
     const int V = backward_vectors(D, kind), narrow = D <= 8 * kVec ? 8 : D <= 16 * kVec ? 16 : D <= 32 * kVec ? 32 : 64;
     const bool wide = D > 64 * kVec;
     const int per = wide ? 1 : 256 / narrow, waves = wide ? norm_threads(D, V) / 64 : 4;
-    const int held = 256 * std::max(1, 4 * backward_waves(kind, f32, V) / waves);
+    int held = std::max(1, 4 * backward_waves(kind, f32, V) / waves);
+    while ((held & (held - 1)) && (kind != kNormPlain || f32 || V > 1)) held &= held - 1;
+    held *= 256;
     return (int32_t)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, held));
 }
 
