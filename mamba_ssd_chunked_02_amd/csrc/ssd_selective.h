@@ -108,9 +108,12 @@ __device__ inline void rows_to_all(float v, float (&to)[4]) {
     swap_rows(to[0], to[1]);
     swap_rows(to[2], to[3]);
 }
-// Row j of the result: the sum of v[j] over the four rows.
+// Row j of the result: the sum of v[j] over the four rows.  A swap takes a register
+// two wait states after a vector instruction wrote it, which the compiler sees to for
+// its own instructions, but not for dot_row's, whose results come here: hence the wait.
 __device__ inline float sum_rows(const float (&v)[4]) {
     float a = v[0], c = v[2], b = v[1], d = v[3];
+    asm("s_nop 1" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
     swap_halves(a, c);
     swap_halves(b, d);
     a += c;
@@ -144,7 +147,8 @@ __device__ inline void in_wave_order() {
 // acc = (FIRST) or acc += src[lane F + j of its row] v[j] for j = 0..3: the
 // multiplication takes its operand across the row, which the compiler does only for
 // plain products (with a move otherwise: 7 cycles in place of 4.6).  The operand must
-// not have been written in the two instructions before.
+// not have been written in the two instructions before; nor may another lane take a
+// result in the two behind (sum_rows waits).
 template <int F, bool FIRST>
 __device__ inline void dot_row4(float& acc, float src, float v0, float v1, float v2, float v3) {
     if constexpr (FIRST)
