@@ -718,6 +718,8 @@ ssd_status ssd_gated_rms_norm_backward(const void* dy, const void* x, const void
  *     mean = mean(out),  rstd = 1 / sqrt(mean((out - mean)^2) + eps)
  *     y    = (out - mean) rstd weight + bias
  * y, mean and rstd come from the fp32 sum, out is that sum rounded to its type.
+ * A row that is not finite has no finite rstd; one whose squared distances overflow
+ * fp32 has an rstd of 0.
  * Shape: an ssd_norm_shape as for the residual norm (groups 1, strides and
  * norm_before_gate 0); without a residual dtype2 is dtype.
  *   x          [rows, D]  dtype

@@ -76,10 +76,12 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void layer_norm_kernel
         }
         p.sum2(rest, ss, lds2);
         rest /= (float)n;
-        const float rstd = 1.f / sqrtf(fmaxf(ss / (float)n - rest * rest, 0.f) + a.eps);
+        // NaN stays NaN; squares that overflow leave rstd at 0, also where the mean's rounding does so, too
+        const float var = ss / (float)n - fminf(rest * rest, 3.4028234e38f);
+        const float rstd = 1.f / sqrtf(__builtin_elementwise_maximum(var, 0.f) + a.eps);
         if (!on) continue;
         if (p.lane == 0) {
-            if (a.mean) a.mean[row] = mean + rest;
+            if (a.mean) a.mean[row] = fabsf(mean) < __builtin_inff() ? mean + rest : mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
 #pragma unroll
