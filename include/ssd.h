@@ -566,7 +566,7 @@ ssd_status ssd_selective_scan_workspace_size(const ssd_selective_shape* shape, i
  *   x, dt        [rows, C]      dtype
  *   A            [C, N]         fp32
  *   B, C         [rows, G, N]   dtype
- *   D            [C]            fp32, or NULL (zero)
+ *   D            [C]            fp32, or NULL (no skip)
  *   z            [rows, C]      dtype, or NULL (no gate)
  *   act          NULL: dt as given; else the activation (its dt_bias [C] or NULL)
  *   init_state   [batch, C, N]  fp32, or NULL (zero)

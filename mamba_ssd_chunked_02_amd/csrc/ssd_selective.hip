@@ -131,7 +131,8 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
                     if constexpr (!LOCAL) y[t] = dot_row<at * NS % 16>(cc[at * NS / 16], h);
                 });
                 if constexpr (!LOCAL) {
-                    float v = sum_rows(y) + D * One<T>::widen(r.x[i]);
+                    float v = sum_rows(y);
+                    if (a.D) v += D * One<T>::widen(r.x[i]);  // not 0 times an infinite x
                     if (gated) {
                         const float z = One<T>::widen(r.z[i]);
                         v *= z * sigmoid_f(z);
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(256) void selective_step_kernel(SelArgs a, const fl
             float v = y[r];
             v += __shfl_xor(v, 1);
             v += __shfl_xor(v, 2);
-            v += D * x[r];
+            if (a.D) v += D * x[r];
             if (a.z) v *= z[r] * sigmoid_f(z[r]);
             if (q != 0 || r >= rows) continue;
             if (a.y_f32) ((float*)a.y)[(s0 + r) * a.C + c] = v;

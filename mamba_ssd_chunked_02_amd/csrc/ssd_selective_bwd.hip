@@ -432,12 +432,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                 if (a.z) {
                     const float z = there ? One<T>::widen(r.z[i]) : 0.f, sg = sigmoid_f(z);
                     u *= z * sg;
-                    dz = dy * (sum_rows(y) + D * x) * (sg * (1.f + z * (1.f - sg)));
+                    float p = sum_rows(y);
+                    if (a.D) p += D * x;
+                    dz = dy * p * (sg * (1.f + z * (1.f - sg)));
                 }
+                float dx = dt[i] * S;
+                if (a.D) dx += D * u;  // not 0 times an infinite u
                 const float draw = there ? (x * S + E) * step.slope(One<T>::widen(r.dt[i]), dt[i]) : 0.f;
                 dbias += draw;
                 dD += u * x;
-                One<T>::store(gx.r, gx.at(4 * i), dt[i] * S + D * u);
+                One<T>::store(gx.r, gx.at(4 * i), dx);
                 One<T>::store(gd.r, gd.at(4 * i), draw);
                 if (a.z) One<T>::store(gz.r, gz.at(4 * i), dz);
                 // the sums over the wave's channels of the registers that are complete
