@@ -317,6 +317,29 @@ struct StepSize {
     }
 };
 
+// ---------------------------------------------------------------- states that are not there
+// A lane's states behind the last one are 0, as their B and C are, and so add nothing to a
+// sum over states -- but for 0 times an infinity, a NaN that would stay.  A tile with such
+// a factor is computed with the masks, which put these states back to 0: forward once
+// more, when the NaN has shown, backward in place of the plain way.
+__device__ inline bool finite(float v) { return fabsf(v) < __builtin_inff(); }
+template <int NS>
+struct There {
+    uint32_t m[NS];
+    __device__ inline There(int N, int q) {
+        asm volatile("" : "+s"(N));  // here, not in front of the loop over tiles, where nobody needs them
+#pragma unroll
+        for (int j = 0; j < NS; ++j) m[j] = q * NS + j < N ? 0xffffffffu : 0u;
+    }
+    __device__ inline float operator()(int j, float v) const {
+        return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & m[j]);
+    }
+};
+struct Everywhere {
+    __device__ inline Everywhere(int, int) {}
+    __device__ inline float operator()(int, float v) const { return v; }
+};
+
 // ---------------------------------------------------------------- items
 __device__ inline int64_t uniform64(int64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);

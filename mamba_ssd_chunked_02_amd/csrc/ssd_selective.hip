@@ -36,12 +36,15 @@ struct RawTile {
 };
 
 // LOCAL: the states that items end with, from zero.  Else y, final and saved states.
-template <typename T, int NS, bool LOCAL>
+// PADDED: some lanes' last states are not there (11 states, 8 x 2048 x 5120: 535 us, 505
+// without looking after them; chosen by a branch in front of each tile 570 to 595).
+template <typename T, int NS, bool LOCAL, bool PADDED>
 __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel(SelArgs a, SelLayout lay, float* ends, float* steps) {
     typedef SelTile<NS> G;
     constexpr int TT = G::TT, NB = G::NB, Q = G::Q;
     // what the rows of a wave hand to each other: step sizes, and they times x
     __shared__ float s_x[kWaves][TT][16][2];
+    __shared__ float s_h[PADDED ? kWaves : 1][NS][64];  // the states entering a tile
     const int lane = threadIdx.x & 63, q = lane >> 4, k = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = a.C / a.G, nblk = (per + kBlockChannels - 1) / kBlockChannels * a.G;
@@ -66,6 +69,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
             A[j] = there ? decay_rate(a.A[chan + s]) : 0.f;
             h[j] = 0.f;
             if (LOCAL) continue;
+            if (PADDED && !there) continue;
             if (e.index > 0) h[j] = ends[((place - 1) * a.C + c) * (4 * NS) + s];
             else if (a.init && there) h[j] = a.init[e.seq * a.C * a.N + chan + s];
         }
@@ -114,34 +118,51 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
                 if (LOCAL) total += dt;
                 *(f32x2*)s_x[wave][4 * i + q][k] = f32x2{dt, dt * One<T>::widen(r.x[i])};
             }
+            if constexpr (PADDED) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j) s_h[wave][j][lane] = h[j];
+            }
             in_wave_order();
-            f32x2 next = *(const f32x2*)s_x[wave][0][k];
-            unroll<Q>([&](auto group) {
-                constexpr int i = decltype(group)::value;
-                float y[4];
-                unroll<4>([&](auto token) {
-                    constexpr int t = decltype(token)::value, at = 4 * i + t;
-                    const f32x2 now = next;  // read one token ahead
-                    if (at + 1 < TT) next = *(const f32x2*)s_x[wave][at + 1 < TT ? at + 1 : 0][k];
-                    unroll<NS>([&](auto state) {
-                        constexpr int j = decltype(state)::value, f = at * NS + j;
-                        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(now[0] * A[j]), h[j],
-                                              row_lane<f % 16>(b[f / 16]) * now[1]);
+            auto tokens = [&](auto careful) {
+                const std::conditional_t<decltype(careful)::value, There<NS>, Everywhere> there(a.N, q);
+                f32x2 next = *(const f32x2*)s_x[wave][0][k];
+                unroll<Q>([&](auto group) {
+                    constexpr int i = decltype(group)::value;
+                    float y[4];
+                    unroll<4>([&](auto token) {
+                        constexpr int t = decltype(token)::value, at = 4 * i + t;
+                        const f32x2 now = next;  // read one token ahead
+                        if (at + 1 < TT) next = *(const f32x2*)s_x[wave][at + 1 < TT ? at + 1 : 0][k];
+                        unroll<NS>([&](auto state) {
+                            constexpr int j = decltype(state)::value, f = at * NS + j;
+                            h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(now[0] * A[j]), h[j],
+                                                  row_lane<f % 16>(b[f / 16]) * now[1]);
+                            h[j] = there(j, h[j]);
+                        });
+                        if constexpr (!LOCAL) y[t] = dot_row<at * NS % 16>(cc[at * NS / 16], h);
                     });
-                    if constexpr (!LOCAL) y[t] = dot_row<at * NS % 16>(cc[at * NS / 16], h);
-                });
-                if constexpr (!LOCAL) {
-                    float v = sum_rows(y);
-                    if (a.D) v += D * One<T>::widen(r.x[i]);  // not 0 times an infinite x
-                    if (gated) {
-                        const float z = One<T>::widen(r.z[i]);
-                        v *= z * sigmoid_f(z);
+                    if constexpr (!LOCAL) {
+                        float v = sum_rows(y);
+                        if (a.D) v = __builtin_fmaf(D, One<T>::widen(r.x[i]), v);  // not 0 times an infinite x
+                        if (gated) {
+                            const float z = One<T>::widen(r.z[i]);
+                            v *= z * sigmoid_f(z);
+                        }
+                        if (a.y_f32) One<float>::store(ty.r, ty.at(4 * i), v);
+                        else One<bf16_t>::store(ty.r, ty.at(4 * i), v);
                     }
-                    if (a.y_f32) One<float>::store(ty.r, ty.at(4 * i), v);
-                    else One<bf16_t>::store(ty.r, ty.at(4 * i), v);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            };
+            tokens(std::false_type{});
+            if constexpr (PADDED) {
+                // the last of them, which is as the others are: 0, or NaN from some token on
+                if (__any(q == 3 && !(h[NS - 1] == 0.f))) {
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) h[j] = s_h[wave][j][lane];
+                    tokens(std::true_type{});
                 }
-                __builtin_amdgcn_sched_barrier(0);
-            });
+            }
             in_wave_order();
             if (!LOCAL) ys.move(TT);
         };
@@ -297,7 +318,7 @@ hipError_t run_scan(const SelArgs& a, const SelLayout& lay, void* ws, hipStream_
     if (work == 0) return hipSuccess;
     const dim3 grid((unsigned)std::min<int64_t>(work, kMaxBlocks)), block(64 * kWaves);
     if (!lay.whole) {
-        hipLaunchKernelGGL((selective_kernel<T, NS, true>), grid, block, 0, stream, a, lay, ends, steps);
+        hipLaunchKernelGGL((selective_kernel<T, NS, true, false>), grid, block, 0, stream, a, lay, ends, steps);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t blocks = ((int64_t)a.C * 4 * NS + 255) / 256 * a.nseq;
@@ -306,7 +327,10 @@ hipError_t run_scan(const SelArgs& a, const SelLayout& lay, void* ws, hipStream_
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((selective_kernel<T, NS, false>), grid, block, 0, stream, a, lay, ends, steps);
+    if (a.N == 4 * NS)
+        hipLaunchKernelGGL((selective_kernel<T, NS, false, false>), grid, block, 0, stream, a, lay, ends, steps);
+    else
+        hipLaunchKernelGGL((selective_kernel<T, NS, false, true>), grid, block, 0, stream, a, lay, ends, steps);
     return hipGetLastError();
 }
 

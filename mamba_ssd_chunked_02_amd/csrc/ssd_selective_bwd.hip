@@ -252,7 +252,8 @@ struct RawBack {
     uint32_t dy[G::Q];
 };
 
-template <typename T, int NS>
+// PADDED: some lanes' last states are not there.
+template <typename T, int NS, bool PADDED>
 __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelArgs a, SelLayout lay, const float* ends,
                                                                          float* part_bc, float* part_a) {
     typedef SelBack<NS> G;
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
             const int s = q * NS + j;
             A[j] = s < a.N ? decay_rate(a.A[chan + s]) : 0.f;
             dA[j] = ga[j] = 0.f;
-            if (e.seq < 0 || !on) continue;
+            if (e.seq < 0 || !on || (PADDED && s >= a.N)) continue;
             if (!e.last) ga[j] = ends[((place + 1) * a.C + c) * (4 * NS) + s];
             else if (a.dfinal && s < a.N) ga[j] = a.dfinal[e.seq * a.C * a.N + chan + s];
         }
@@ -333,10 +334,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
         auto advance = [&](const RawBack<T, NS>& r) {
             float b[NB];
             bs.widen(r.b, b);
+            bool wild = false;
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
-                const float dt = step(One<T>::widen(r.dt[i]));
-                *(f32x2*)&s_x[wave][4 * i + q][k] = f32x2{dt, on ? dt * One<T>::widen(r.x[i]) : 0.f};
+                const float dt = step(One<T>::widen(r.dt[i])), dtx = on ? dt * One<T>::widen(r.x[i]) : 0.f;
+                *(f32x2*)&s_x[wave][4 * i + q][k] = f32x2{dt, dtx};
+                if (PADDED) wild = wild || !finite(dtx);
             }
             in_wave_order();
             f32x2 next = *(const f32x2*)&s_x[wave][0][k];  // read one token ahead
@@ -352,26 +355,41 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                 __builtin_amdgcn_sched_barrier(0);
             });
             in_wave_order();
+            if (PADDED && __any(wild)) {
+                const There<NS> there(a.N, q);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) h[j] = there(j, h[j]);
+            }
         };
-        // gradients of the tile whose first row of the item is t0, `left` tokens of it, h
-        // the states entering it
-        auto tile = [&](int t0, int left, const RawBack<T, NS>& r, auto tail) {
-            constexpr bool TAIL = decltype(tail)::value;
-            float b[NB], cc[NB], dt[Q];
-            bs.widen(r.b, b);
-            cs.widen(r.c, cc);
+        // What the rows of a wave hand to each other of a tile, `left` tokens of it.  PADDED: whether it is finite.
+        float dt[Q];
+        auto hand_over = [&](int left, const RawBack<T, NS>& r, auto tail) {
+            bool wild = false;
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
-                const bool there = on && (!TAIL || 4 * i + q < left);
+                const bool there = on && (!decltype(tail)::value || 4 * i + q < left);
                 dt[i] = there ? step(One<T>::widen(r.dt[i])) : 0.f;
                 float u = widen_either(r.dy[i], a.y_f32);
                 if (a.z) {
                     const float z = One<T>::widen(r.z[i]);
                     u *= z * sigmoid_f(z);
                 }
-                s_x[wave][4 * i + q][k] = f32x4{dt[i], there ? dt[i] * One<T>::widen(r.x[i]) : 0.f, there ? u : 0.f, 0.f};
+                const f32x4 to = f32x4{dt[i], there ? dt[i] * One<T>::widen(r.x[i]) : 0.f, there ? u : 0.f, 0.f};
+                s_x[wave][4 * i + q][k] = to;
+                if (PADDED) wild = wild || !finite(to[1]) || !finite(to[2]);
             }
             in_wave_order();
+            return !(PADDED && __any(wild));
+        };
+        // gradients of the tile whose first row of the item is t0, `left` tokens of it, h
+        // the states entering it.  TAIL: less than TT of them, or factors that are not finite
+        auto tile = [&](int t0, int left, const RawBack<T, NS>& r, auto tail) {
+            constexpr bool TAIL = decltype(tail)::value;
+            const std::conditional_t<TAIL && PADDED, There<NS>, Everywhere> state_there(a.N, q);
+            float b[NB], cc[NB];
+            bs.widen(r.b, b);
+            cs.widen(r.c, cc);
+            if constexpr (!PADDED) hand_over(left, r, tail);
             float before[TT][NS], decay[TT][NS];
             f32x4 next = s_x[wave][0][k];
             __builtin_amdgcn_sched_barrier(0);
@@ -384,8 +402,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                     before[t][j] = h[j];
                     decay[t][j] = 1.f;
                     if (TAIL && t >= left) return;
-                    decay[t][j] = __builtin_amdgcn_exp2f(here[0] * A[j]);
-                    h[j] = __builtin_fmaf(decay[t][j], h[j], row_lane<f % 16>(b[f / 16]) * here[1]);
+                    decay[t][j] = state_there(j, __builtin_amdgcn_exp2f(here[0] * A[j]));
+                    h[j] = state_there(j, __builtin_fmaf(decay[t][j], h[j], row_lane<f % 16>(b[f / 16]) * here[1]));
                 });
                 __builtin_amdgcn_sched_barrier(0);
             });
@@ -410,6 +428,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                     // h: the states behind this token, ga: the adjoint in front of the next one
                     float vb[NS], vc[NS];
                     add_row<F>(ga, cc[at * NS / 16], here[2]);
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) ga[j] = state_there(j, ga[j]);
                     y[t] = dot_row<F>(cc[at * NS / 16], h);
                     s[t] = dot_row<F>(b[at * NS / 16], ga);
 #pragma unroll
@@ -433,11 +453,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                     const float z = there ? One<T>::widen(r.z[i]) : 0.f, sg = sigmoid_f(z);
                     u *= z * sg;
                     float p = sum_rows(y);
-                    if (a.D) p += D * x;
+                    if (a.D) p = __builtin_fmaf(D, x, p);
                     dz = dy * p * (sg * (1.f + z * (1.f - sg)));
                 }
                 float dx = dt[i] * S;
-                if (a.D) dx += D * u;  // not 0 times an infinite u
+                if (a.D) dx = __builtin_fmaf(D, u, dx);  // not 0 times an infinite u
                 const float draw = there ? (x * S + E) * step.slope(One<T>::widen(r.dt[i]), dt[i]) : 0.f;
                 dbias += draw;
                 dD += u * x;
@@ -541,8 +561,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                     }
                     move(-TT);
                 }
-                if (t + TT <= here) tile(chunk + t, TT, cur, std::false_type{});
-                else tile(chunk + t, here - t, cur, std::true_type{});
+                const bool whole = t + TT <= here;
+                if constexpr (PADDED) {
+                    const bool tame = whole ? hand_over(TT, cur, std::false_type{}) : hand_over(here - t, cur, std::true_type{});
+                    if (whole && tame) tile(chunk + t, TT, cur, std::false_type{});
+                    else tile(chunk + t, min(here - t, TT), cur, std::true_type{});
+                } else {
+                    if (whole) tile(chunk + t, TT, cur, std::false_type{});
+                    else tile(chunk + t, here - t, cur, std::true_type{});
+                }
             }
             move(TT - (int)kSelStateRows);
         }
@@ -616,8 +643,11 @@ hipError_t run_backward(const SelArgs& a, const SelLayout& lay, void* ws, hipStr
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         const int64_t work = lay.places * lay.blocks_bc * a.G;
-        hipLaunchKernelGGL((selective_backward_kernel<T, NS>), dim3((unsigned)std::min<int64_t>(work, kMaxBlocks)),
-                           dim3(64 * kWaves), 0, stream, a, lay, ends, part_bc, part_a);
+        const dim3 grid((unsigned)std::min<int64_t>(work, kMaxBlocks)), block(64 * kWaves);
+        if (a.N == 4 * NS)
+            hipLaunchKernelGGL((selective_backward_kernel<T, NS, false>), grid, block, 0, stream, a, lay, ends, part_bc, part_a);
+        else
+            hipLaunchKernelGGL((selective_backward_kernel<T, NS, true>), grid, block, 0, stream, a, lay, ends, part_bc, part_a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (a.T > 0) {
             const int64_t elements = a.T * a.G * 2 * a.N;
