@@ -373,10 +373,23 @@ __device__ inline void carry(float* p, int64_t dp, const float* steps, int64_t d
             v[j] = p[o * dp];
             a[j] = steps[o * ds];
         }
+        const float in = h;
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             if (j >= n) break;
             h = __builtin_fmaf(__builtin_amdgcn_exp2f(A * a[j]), h, v[j]);
+            p[j * dp] = h;
+        }
+        // An item's factor may underflow or overflow where no token's does, but is a positive
+        // number: 0 and infinity pass it as they are.  Looked into where a NaN came of it.
+        if (h == h) continue;
+        h = in;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (j >= n) break;
+            const float e = A * a[j];
+            const bool kept = (h == 0.f || fabsf(h) == __builtin_inff()) && fabsf(e) < __builtin_inff();
+            h = kept ? h + v[j] : __builtin_fmaf(__builtin_amdgcn_exp2f(e), h, v[j]);
             p[j * dp] = h;
         }
     }
