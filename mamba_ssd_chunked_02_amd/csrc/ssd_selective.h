@@ -279,10 +279,12 @@ __device__ inline float widen_either(uint32_t v, bool f32) {
 }
 
 // ---------------------------------------------------------------- step sizes
-// log2(e) A, the factor of the step size in a decay's exponent.  Kept finite below, so
+// log2(e) A, the factor of the step size in a decay's exponent.  Kept finite, so
 // that a step of 0 leaves the state as it is whatever A is: a tile's rows behind the
 // last token take such steps.  NaN stays NaN.
-__device__ inline float decay_rate(float A) { return __builtin_elementwise_maximum(A * kLog2e, -3.4028234e38f); }
+__device__ inline float decay_rate(float A) {
+    return __builtin_elementwise_minimum(__builtin_elementwise_maximum(A * kLog2e, -3.4028234e38f), 3.4028234e38f);
+}
 
 // softplus(v) = max(v, 0) + log(1 + u), u = exp(-|v|): 13 operations, off by 2.4 of
 // 2^-24 for v >= 0, 7 for v > -15, 9 for v > -30 (measured on 2^22 values).  The

@@ -76,6 +76,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
         const StepSize step(a.act, c);
         const float D = !LOCAL && a.D ? a.D[c] : 0.f;
         float total = 0.f;
+        uint32_t decays = q == 0 ? 0 : ~0u;  // LOCAL: the first token has nothing to decay, be its factor infinite
 
         const bool gated = !LOCAL && a.z;
         typedef RowsOf<TT> Rows;
@@ -116,7 +117,9 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
                 float dt = step(One<T>::widen(r.dt[i]));
                 if (left < TT) dt = 4 * i + q < left ? dt : 0.f;
                 if (LOCAL) total += dt;
-                *(f32x2*)s_x[wave][4 * i + q][k] = f32x2{dt, dt * One<T>::widen(r.x[i])};
+                const float dtx = dt * One<T>::widen(r.x[i]);
+                if (LOCAL && i == 0) dt = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, dt) & decays);
+                *(f32x2*)s_x[wave][4 * i + q][k] = f32x2{dt, dtx};
             }
             if constexpr (PADDED) {
 #pragma unroll
@@ -164,6 +167,7 @@ __global__ __launch_bounds__(64 * kWaves, NS <= 4 ? 6 : 4) void selective_kernel
                 }
             }
             in_wave_order();
+            decays = ~0u;
             if (!LOCAL) ys.move(TT);
         };
         RawTile<T, NS> cur, nxt;
