@@ -599,8 +599,9 @@ ssd_status ssd_selective_scan(const void* x, const void* dt, const float* A, con
  *   ddt_bias     [C]            fp32, or NULL (not written); needs act's dt_bias
  *   dinit_state  [batch, C, N]  fp32, or NULL (not written); not dfinal_state
  * The other arguments as given to the forward pass, states as written by it.
- * Sums over tokens and channels are fp32, in an order that depends on the shape
- * alone.  Same errors.
+ * init_state is checked and not read (each sequence's first saved state is it):
+ * NULL gives the same.  Sums over tokens and channels are fp32, in an order that
+ * depends on the shape alone.  Same errors.
  */
 ssd_status ssd_selective_scan_backward(const void* dy, const float* dfinal_state, const void* x, const void* dt,
                                        const float* A, const void* B, const void* C, const float* D, const void* z,

@@ -267,7 +267,7 @@ struct SelArgs {
     const void* Cm;            // [rows, G, N]
     const float* A;            // [C, N]
     const float* D;            // [C] or NULL
-    const float* init;         // [nseq, C, N] or NULL (zero)
+    const float* init;         // [nseq, C, N] or NULL (zero); forward
     int64_t x_stride, dt_stride, z_stride, b_stride, c_stride;
     const int32_t* cu;         // device [nseq+1] or NULL (dense)
     int64_t nseq, L, T;

@@ -177,7 +177,6 @@ SSD_API ssd_status ssd_selective_scan_backward(const void* dy, const float* dfin
     a.Cm = C;
     a.A = A;
     a.D = D;
-    a.init = init_state;
     a.states_in = states;
     a.dx = dx;
     a.ddt = ddt;

@@ -154,7 +154,8 @@ def selective_scan_backward(dy, x, dt, A, B, C, states, D=None, z=None, *, dt_so
                             dz=None, want_dinit: bool = True, dinit_state=None, workspace=None):
     """Gradients of selective_scan for dy (fp32 or bf16, shaped as x) and
     ``dfinal_state`` [b, C, N] fp32 (None: zero).  The other arguments as given to
-    selective_scan, ``states`` as returned by it.
+    selective_scan, ``states`` as returned by it; they hold ``init_state``, which is
+    checked and not read.
 
     Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinit_state), ddt that of the
     raw step sizes; dD, dz and ddt_bias are None without D, z and dt_bias.  dx,
