@@ -106,8 +106,10 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void layer_norm_kernel
 // three, since the compiler at four waits for its loads early (65536 x 2560 bf16: 281
 // us, four 347; with an fp32 residual 480, 519), and with a scale none of the next row's
 // (527; with them 685, four waves without them 610).  fp32 without a residual: three
-// for one vector a lane (65536 x 1024: 138, four 149), four for two (16384 x 5120: 176,
-// three 208); bf16 four (16384 x 4096: 83, three 108; 16384 x 8192 147, three with the next row 180).
+// for one vector a lane (65536 x 1024: 138, four 149), four for two (16384 x 5120: 176
+// with 3 of them in scratch, three 208); bf16 four (16384 x 4096: 83, three 108; 16384 x 8192 147, three with the next row 180).
+// Four vectors a lane, over 8192 columns, do not fit with a residual: 11 to 19 registers go
+// to scratch (8192 x 12288 bf16 246 us, 4.1 TB/s), with a scale 74 to 100 (513 us, 2.4).
 constexpr int backward_waves(int kind, bool f32, int V) {
     return kind == kNormPlain && V <= 2 ? (V == 1 && f32 ? 3 : 4) : V == 1 ? 3 : 2;
 }
@@ -300,10 +302,14 @@ hipError_t backward_by_columns(const NormArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Workgroups along the rows of the backward pass: what 256 compute units hold at once,
-// no more than there are rows for.  Of each a power of two, so that rows divide evenly
-// (16384 x 5120 bf16: 2 102 us, 3 126; fp32 176, 200; 65536 x 1024 with an fp32 residual
-// 4 189, 6 209), but all of them for bf16 rows without a residual by one vector, which
-// have the least in flight (32768 x 2560: 3 99, 2 121; 65536 x 1536: 5 112, 4 120).
+// no more than there are rows for.  By registers 16 waves are three workgroups of 5 waves,
+// but a third one does not start beside two: of 768 over 5120 columns 256 started when the
+// others ended.  Hence a power of two of each compute unit: 65536 x 5120 without a residual
+// 2 332 us, 3 399, fp32 676 and 748.  Where they all start at once it is quicker, too, for a
+// reason not known: 65536 x 1024 with an fp32 residual 4 186 us, 6 206, fp32 137 and 144; but
+// not for bf16 rows without a residual by one vector, which have the least in flight and
+// take all of them: 65536 x 2560 3 184 us, 2 227; x 1536 5 111, 4 120.  The quicker side
+// is the same one for 12000, 16384, 20011, 24000, 32768 and 50000 rows.
 int32_t layer_norm_parts(int64_t rows, int32_t D, int kind, bool f32) {
     const int V = backward_vectors(D, kind), narrow = D <= 8 * kVec ? 8 : D <= 16 * kVec ? 16 : D <= 32 * kVec ? 32 : 64;
     const bool wide = D > 64 * kVec;

@@ -145,7 +145,7 @@ struct Team {
         }
         return v;
     }
-    // Two sums; lds holds kMaxWaves pairs.
+    // Two sums; lds holds a pair for each wave of the workgroup.
     __device__ void sum2(float& u, float& v, float (*lds)[2]) const {
 #pragma unroll
         for (int d = 1; d < LANES; d <<= 1) {

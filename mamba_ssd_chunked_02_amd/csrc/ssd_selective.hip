@@ -8,12 +8,14 @@
 // (an item multiplies the state entering it by exp(A S)), a third writes y.  Where
 // the sequences alone fill the chip only the third runs.
 //
-// At 16 states the vector ALU bounds it, not HBM: 8.2 instructions a (token, channel,
+// At 16 states the vector ALU bounds it, not HBM: 8.3 instructions a (token, channel,
 // state) here and 5.5 in the first launch, of which the exponential takes 8.4 cycles a
-// wave, its argument's product, the state's and y's 4 to 4.6 each.  Packed 49152
-// x 8192 x 16, bf16: y 1.64 ms (2.6 GB read, 0.86 written), the end states 1.10; 8 x
-// 2048 x 5120 x 16 as a whole 535 us, 2.5 T states a second where 8 waves a SIMD reach
-// 3.7: 2560 waves on 1024 SIMDs.  A wave's lanes are 16 channels by four quarters of
+// wave, its argument's product, the state's and y's 4 to 4.6 each.  Some are the
+// compiler's: of 281 vector instructions in the loop over tiles 24 are moves and 9 lane
+// reads of spilled scalars; the bf16 kernels for up to 4 states also keep 3 to 5
+// registers in scratch.  Packed 49152 x 8192 x 16, bf16: y 1.67 ms (2.6 GB read, 0.86
+// written), the end states 1.12; 8 x 2048 x 5120 x 16 as a whole 540 us, 2.5 T states a
+// second where 8 waves a SIMD reach 3.7: 2560 waves on 1024 SIMDs.  A wave's lanes are 16 channels by four quarters of
 // the states: by channel alone a lane would need 16 states, 64 channels' waves and
 // so four times the items, by state alone every load would serve one channel.
 #include <algorithm>
@@ -376,11 +378,12 @@ SelLayout sel_layout(const SelArgs& a, bool backward) {
     const int padded = a.N <= 4 ? 4 : a.N <= 8 ? 8 : a.N <= 16 ? 16 : a.N <= 32 ? 32 : 64;
     auto up = [](int64_t v) { return std::max<int64_t>((v + kSelStateRows - 1) / kSelStateRows, 1) * kSelStateRows; };
     // Forward: sequences of one length that bring 2 waves a SIMD go as a whole (8 x 2048 x
-    // 5120: 564 us; cut into 512 tokens 640), else items for 16 waves a SIMD, so that their
-    // unequal ends even out (packed 49152 x 8192: 1024 tokens 2.98 ms, 512 3.04, 2048 3.02,
-    // 6144 3.31), but 128 tokens at least (4096 x 1536: 64 and 128 tokens 75 us, 256 96; 64
-    // take twice the workspace).  Backward: always items, since no sequence count that is
-    // common fills two waves a SIMD evenly (8 x 2048 x 5120 in items 1.93 ms, whole 2.23).
+    // 5120 forward and backward 2.48 ms; cut into 512 tokens forward 2.54), else items for 16
+    // waves a SIMD, so that their unequal ends even out (packed 49152 x 8192: 512 and 1024
+    // tokens 2.65 ms, 1536, which the rule takes, 2.66, 2048 2.68, 6144 3.07), but 128 tokens
+    // at least (4096 x 1536: 64 and 128 tokens 69 us, 256 91; 64 take twice the workspace).
+    // Backward: always items, since no sequence count that is common fills two waves a SIMD
+    // evenly (8 x 2048 x 5120 forward and backward 2.48 ms, whole 2.79).
     const int64_t least = backward ? 64 : 128;
     if (!backward && !a.cu && a.nseq * waves >= 2048) l.item = up(a.L);
     else l.item = std::max(least, up((int64_t)((double)a.T * waves / 16384)));

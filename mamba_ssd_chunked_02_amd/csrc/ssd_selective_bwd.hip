@@ -12,14 +12,18 @@
 // more than 16), which a lane keeps in LDS, then a tile's, which it keeps in registers
 // with the decays.
 //
-// The vector ALU bounds it: 33.5 instructions a (token, channel, state) in the gradients'
-// kernel: 4 for states and decays, 3.5 for the states once more in front of that, 9 for
-// the adjoint, the products and their sums over states and tokens, 3 for dB's and dC's
-// sums over channels; the rest belongs to a (token, channel).  It holds 208 registers,
-// so two waves a SIMD, and is busy 80% of their cycles.  8 x 2048 x 5120 x 16, bf16:
-// 1.62 ms, the adjoints 0.24, the sums 0.06.  Three waves a SIMD spill (2.56 against
-// 2.0 ms at that time), as do two channels a lane; fp32 matrix products for the sums
-// over channels do not run beside the vector ALU.
+// The vector ALU bounds it: 33.7 instructions a (token, channel, state) in the gradients'
+// kernel for 16 states: 4 for states and decays, 3.5 for the states once more in front of
+// that, 9 for the adjoint, the products and their sums over states and tokens, 3 for dB's
+// and dC's sums over channels; the rest belongs to a (token, channel) or is the compiler's:
+// of 1764 vector instructions in the loop over tiles (two forms of a tile) 207 are moves
+// and 89 lane reads of spilled scalars, of 1605 in that over chunks 40 and 168.  It holds
+// 208 registers, so two waves a SIMD, and is busy 80% of their cycles.  8 x 2048 x 5120 x
+// 16, bf16: 1.62 ms, the adjoints 0.25, the sums 0.06.  Three waves a SIMD spill (2.56
+// against 2.0 ms at that time), as do two channels a lane; fp32 matrix products for the
+// sums over channels do not run beside the vector ALU.  For 33 to 64 states two waves
+// spill as well, 64 to 71 registers of a lane: 0.53 T states a second, where 16 states
+// reach 0.70.
 #include <algorithm>
 #include <type_traits>
 
