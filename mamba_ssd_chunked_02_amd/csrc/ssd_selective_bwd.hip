@@ -462,7 +462,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void selective_backward_kernel(SelA
                 }
                 float dx = dt[i] * S;
                 if (a.D) dx = __builtin_fmaf(D, u, dx);  // not 0 times an infinite u
-                const float draw = there ? (x * S + E) * step.slope(One<T>::widen(r.dt[i]), dt[i]) : 0.f;
+                const float slope = step.slope(One<T>::widen(r.dt[i]), dt[i]);
+                float draw = there ? (x * S + E) * slope : 0.f;
+                if (step.cut && slope == 0.f) draw = 0.f;  // of an infinite gradient, too
                 dbias += draw;
                 dD += u * x;
                 One<T>::store(gx.r, gx.at(4 * i), dx);
