@@ -168,7 +168,7 @@ __device__ inline void dot_row4(float& acc, float src, float v0, float v1, float
             : "+v"(acc)
             : "v"(src), "v"(v0), "v"(v1), "v"(v2), "v"(v3), "n"(F), "n"(F + 1), "n"(F + 2), "n"(F + 3));
 }
-// acc_j += src[lane F + j of its row] v.
+// acc_j += src[lane F + j of its row] v; the results as dot_row4's.
 template <int F>
 __device__ inline void add_row4(float& a0, float& a1, float& a2, float& a3, float src, float v) {
     asm("s_nop 1\n\t"

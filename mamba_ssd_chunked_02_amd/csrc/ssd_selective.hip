@@ -14,10 +14,11 @@
 // compiler's: of 281 vector instructions in the loop over tiles 24 are moves and 9 lane
 // reads of spilled scalars; the bf16 kernels for up to 4 states also keep 3 to 5
 // registers in scratch.  Packed 49152 x 8192 x 16, bf16: y 1.58 to 1.67 ms (2.6 GB read,
-// 0.86 written), the end states 1.06 to 1.12; 8 x 2048 x 5120 x 16 as a whole 540 us, 2.5 T states a
-// second where 8 waves a SIMD reach 3.7: 2560 waves on 1024 SIMDs.  A wave's lanes are 16 channels by four quarters of
-// the states: by channel alone a lane would need 16 states, 64 channels' waves and
-// so four times the items, by state alone every load would serve one channel.
+// 0.86 written), the end states 1.06 to 1.12; 8 x 2048 x 5120 x 16 as a whole 540 us,
+// 2.5 T states a second where 8 waves a SIMD reach 3.7: 2560 waves on 1024 SIMDs.  A
+// wave's lanes are 16 channels by four quarters of the states: by channel alone a lane
+// would need 16 states, 64 channels' waves and so four times the items, by state alone
+// every load would serve one channel.
 #include <algorithm>
 #include <type_traits>
 
